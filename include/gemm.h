@@ -446,6 +446,147 @@ GEMM_API void gemm_tuning_clear(void);
 GEMM_API gemm_status gemm_tuning_save(const char *path);
 GEMM_API int32_t gemm_tuning_load(const char *path);
 
+/* ------------------------------------------------------------------------
+ * Products of a sparse expert layer: fp8 operands with a scale for each
+ * block of 128 values, products grouped by expert, and the norm that feeds
+ * them.  As everywhere in this library: row-major operands, device pointers,
+ * work enqueued on `stream`, nothing allocated and nothing kept between
+ * calls, argument errors before any HIP call.  Results are deterministic
+ * (no atomics).  These calls have no forced kernels and no tuning entries.
+ * ---------------------------------------------------------------------- */
+
+#define GEMM_SCALE_BLOCK 128
+
+/*
+ * Block quantisation to OCP E4M3.  X is M x K, fp32 (GEMM_DTYPE_F32) or bf16
+ * (GEMM_DTYPE_BF16F32).  block_rows 1 gives every 128 consecutive columns of
+ * a row a scale (an activation's layout), block_rows 128 every 128 x 128
+ * tile (a weight's); blocks at the edges are cut.  With amax the largest
+ * magnitude among a block's finite values:
+ *
+ *     scale = max(amax, 2^-100) / 448          Q = e4m3(x / scale)
+ *
+ * rounded to nearest even, the quotient taken as x * (448 / max(amax,
+ * 2^-100)) in fp32.  Infinities and NaN become the NaN code and do not
+ * count in amax.  Row i of Q starts at Q + i*ldq (ldq >= K); the scale of row
+ * block i and column block j is scales[i*lds + j] (lds >= ceil(K / 128),
+ * ceil(M / block_rows) rows).  The matrix-core paths of the products below
+ * need rows of Q on 16 bytes: a multiple of 16 for ldq.
+ */
+GEMM_API gemm_status gemm_quantize(int32_t dtype, int32_t block_rows, int64_t M, int64_t K,
+                                   const void *X, int64_t ldx, uint8_t *Q, int64_t ldq,
+                                   float *scales, int64_t lds, gemm_stream_t stream);
+
+/*
+ * Root-mean-square norm over rows of N values, with the residual's addition.
+ *
+ *     s = round(x + residual)                          (x, if residual is NULL)
+ *     y = s * (mean over the row of s^2 + eps)^-1/2 * weight
+ *
+ * X, residual, sum and weight (N values) are of type dtype (fp32 or bf16);
+ * s is rounded to that type, as it is stored, before its square is taken,
+ * so that the backward pass below sees the values the norm saw.  Squares and
+ * sums are fp32.  sum receives s (NULL: not stored); it may be X or residual
+ * itself.  out_type GEMM_OUT_F32 and GEMM_OUT_BF16 store y (rounded once);
+ * GEMM_OUT_FP8 stores codes and writes scales[i*ld_scales + j] for columns
+ * 128j .. of row i, as gemm_quantize with block_rows 1 does of y before
+ * any rounding (scales is not used otherwise).  out overlaps no input.
+ * N == 0 writes nothing.
+ */
+GEMM_API gemm_status gemm_rms_norm(int32_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx,
+                                   const void *residual, int64_t ldr, const void *weight, float eps,
+                                   void *sum, int64_t ld_sum, int32_t out_type, void *out, int64_t ldo,
+                                   float *scales, int64_t ld_scales, gemm_stream_t stream);
+
+/*
+ * Gradients of gemm_rms_norm, from dY (the gradient of y), the stored sum S
+ * and dS, the gradient that reaches S past the norm (NULL: none), all of type
+ * dtype.  With r = (mean(s^2) + eps)^-1/2 of a row and g = dy * weight:
+ *
+ *     dX = r * (g - s * r^2 * mean(g * s)) + dS        (of X and of the residual)
+ *     dweight[j] = sum over rows of dy * s * r          (fp32)
+ *
+ * dX may be dY or dS itself.  dweight may be NULL (not wanted); otherwise
+ * `workspace` holds at least gemm_rms_norm_workspace_size(M, N) bytes
+ * (4-byte aligned, contents need no clearing) and GEMM_ERR_SCRATCH is
+ * returned if it does not.  A quantised forward output passes its gradient
+ * straight through.
+ */
+GEMM_API int64_t gemm_rms_norm_workspace_size(int64_t M, int64_t N);
+GEMM_API gemm_status gemm_rms_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, int64_t lddy,
+                                            const void *S, int64_t lds, const void *weight, float eps,
+                                            const void *dS, int64_t ldds, void *dX, int64_t lddx,
+                                            float *dweight, void *workspace, int64_t workspace_bytes,
+                                            gemm_stream_t stream);
+
+/*
+ * Scales of fp8 operands, one for each 128 values along k: of A per row,
+ * of B per 128 columns of the product.  In elements of float:
+ *   scale of A[i][128j ..]                  a[i*a_row + j*a_block]
+ *   scale of group g's B, k block j, columns 128t ..   b[g*b_group + t*b_n + j*b_k]
+ * Any strides (>= 0) are taken: 0 shares a scale along that direction (a
+ * per-tensor scale has all of them 0).
+ */
+typedef struct gemm_block_scales {
+    const float *a;
+    int64_t a_row, a_block;
+    const float *b;
+    int64_t b_n, b_k, b_group;
+} gemm_block_scales;
+
+/*
+ * fp8 product with block scales:
+ *
+ *     out[i][j] = alpha * sum over blocks t of a(i, t) * b(t, j) * (sum over k in block t of A[i][k] * B[k][j])
+ *
+ * A is M x K E4M3.  op_b GEMM_OP_T: B is stored N x K (a linear layer's
+ * weights); GEMM_OP_N: K x N, so the weights of a layer and their scales,
+ * with b_n and b_k exchanged, serve its input gradient as they are stored.
+ * out is fp32 (GEMM_OUT_F32) or bf16.  Block sums are the fp8 matrix core's
+ * (see "fp8 accuracy" above); they are scaled and added in fp32.
+ * K == 0 or alpha == 0 gives zeros and reads no operand.
+ */
+GEMM_API gemm_status gemm_block_scaled(int32_t op_b, int64_t M, int64_t N, int64_t K, float alpha,
+                                       const uint8_t *A, int64_t lda, const uint8_t *B, int64_t ldb,
+                                       const gemm_block_scales *scales, int32_t out_type, void *out, int64_t ldo,
+                                       gemm_stream_t stream);
+
+/*
+ * Products grouped by expert.  Group g owns rows ends[g-1] .. ends[g]-1 of A
+ * and of out (row 0 on for g = 0); its operand B is at B + g*stride_b
+ * elements:
+ *
+ *     out[i][:] = alpha * A[i][:] x B_g          for every row i of group g
+ *
+ * ends is a device array of `groups` 32-bit row numbers, nondecreasing, at
+ * most M; it is read on the device, so no host wait is needed between a
+ * router and this call.  A group may own no row.  Rows from the last end on
+ * become zero.  (Values out of order or past M are clamped to the running
+ * maximum and to M: no row outside 0 .. M-1 is ever touched.)  dtype is any
+ * gemm_dtype; fp8 takes block scales as above, the others a NULL `scales`.
+ * op_b and the output types are those of gemm_block_scaled.
+ *
+ * gemm_grouped_wgrad sums over each group's rows instead (fp32 or bf16
+ * operands, fp32 result): with dY of M x N and X of M x K,
+ *
+ *     dW_g[n][k] = alpha * sum over rows i of group g of dY[i][n] * X[i][k] + beta * dW_g[n][k]
+ *
+ * at dW + g*stride_w (row n at n*ldw).  A group without rows gives beta * dW
+ * (zeros when beta == 0, whatever dW held).  Rows from the last end on are
+ * not read.
+ */
+GEMM_API gemm_status gemm_grouped(int32_t dtype, int32_t op_b, int32_t groups, const int32_t *ends,
+                                  int64_t M, int64_t N, int64_t K, float alpha,
+                                  const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
+                                  const gemm_block_scales *scales, int32_t out_type, void *out, int64_t ldo,
+                                  gemm_stream_t stream);
+
+GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int32_t *ends,
+                                        int64_t M, int64_t N, int64_t K, float alpha,
+                                        const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                                        float beta, float *dW, int64_t ldw, int64_t stride_w,
+                                        gemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

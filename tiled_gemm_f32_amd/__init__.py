@@ -18,7 +18,10 @@ from ._lib import (  # noqa: F401  (re-exported C ABI)
     gemm_bf16f32_ex, gemm_bf16f32_ws, gemm_f32, gemm_f32_ex, gemm_f32_ws, gemm_kernel_count, gemm_kernel_query,
     gemm_plan_query, gemm_status_string, gemm_workspace_size, gemm_autotune, gemm_autotune_general, gemm_tuning_count,
     gemm_tuning_clear, gemm_tuning_save, gemm_tuning_load, load, gemm_general_noalloc, GEMM_ERR_SCRATCH,
-    GEMM_STATIC_SCRATCH_BYTES)
+    GEMM_STATIC_SCRATCH_BYTES, GEMM_SCALE_BLOCK, BlockScales, gemm_quantize, gemm_rms_norm,
+    gemm_rms_norm_workspace_size, gemm_rms_norm_backward, gemm_block_scaled, gemm_grouped, gemm_grouped_wgrad)
+from .experts import (  # noqa: F401
+    block_gemm, grouped_gemm, grouped_wgrad, quantize, rms_norm, rms_norm_backward)
 
 __all__ = ["gemm", "gemm_f32", "gemm_bf16f32", "gemm_f32_ex", "gemm_bf16f32_ex", "gemm_f32_ws", "gemm_bf16f32_ws",
            "gemm_f32_epi", "gemm_bf16f32_epi", "Epilogue", "GEMM_ACT_NONE", "GEMM_ACT_RELU", "GEMM_ACT_GELU",
@@ -28,7 +31,10 @@ __all__ = ["gemm", "gemm_f32", "gemm_bf16f32", "gemm_f32_ex", "gemm_bf16f32_ex",
            "gemm_plan_query", "GemmError", "kernels", "workspace", "autotune", "gemm_autotune",
            "gemm_autotune_general", "gemm_tuning_count",
            "gemm_tuning_clear", "gemm_tuning_save", "gemm_tuning_load", "gemm_general_noalloc",
-           "GEMM_ERR_SCRATCH", "GEMM_STATIC_SCRATCH_BYTES"]
+           "GEMM_ERR_SCRATCH", "GEMM_STATIC_SCRATCH_BYTES", "GEMM_SCALE_BLOCK", "BlockScales",
+           "gemm_quantize", "gemm_rms_norm", "gemm_rms_norm_workspace_size", "gemm_rms_norm_backward",
+           "gemm_block_scaled", "gemm_grouped", "gemm_grouped_wgrad",
+           "block_gemm", "grouped_gemm", "grouped_wgrad", "quantize", "rms_norm", "rms_norm_backward"]
 
 
 def _ld(t, what: str) -> int:

@@ -50,7 +50,11 @@ EXPORTED = ("gemm_f32", "gemm_bf16f32", "gemm_status_string", "gemm_kernel_count
             "gemm_workspace_size", "gemm_f32_ws", "gemm_bf16f32_ws", "gemm_autotune", "gemm_tuning_count",
             "gemm_tuning_clear", "gemm_tuning_save", "gemm_tuning_load", "gemm_f32_epi", "gemm_bf16f32_epi",
             "gemm_general", "gemm_plan_query_general", "gemm_plan_query_epi", "gemm_autotune_general",
-            "gemm_general_noalloc")
+            "gemm_general_noalloc", "gemm_quantize", "gemm_rms_norm", "gemm_rms_norm_workspace_size",
+            "gemm_rms_norm_backward", "gemm_block_scaled", "gemm_grouped", "gemm_grouped_wgrad")
+
+# Values along k (and columns of B) that share a block scale.
+GEMM_SCALE_BLOCK = 128
 
 
 class KernelInfo(ctypes.Structure):
@@ -72,6 +76,12 @@ class Epilogue(ctypes.Structure):
     the output (type, device pointer, leading dimension, scale; type 0 = C)."""
     _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32),
                 ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("out_scale", ctypes.c_float)]
+
+
+class BlockScales(ctypes.Structure):
+    """gemm_block_scales: device pointers to the scales of A and of B and their strides in floats."""
+    _fields_ = [("a", ctypes.c_void_p), ("a_row", ctypes.c_int64), ("a_block", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("b_n", ctypes.c_int64), ("b_k", ctypes.c_int64), ("b_group", ctypes.c_int64)]
 
 
 def _epi(epilogue):
@@ -151,6 +161,19 @@ def load() -> ctypes.CDLL:
     lib.gemm_tuning_save.restype = ctypes.c_int
     lib.gemm_tuning_load.argtypes = [ctypes.c_char_p]
     lib.gemm_tuning_load.restype = i32
+    scales = ctypes.POINTER(BlockScales)
+    lib.gemm_quantize.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_rms_norm.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, i32, vp, i64, vp, i64, vp]
+    lib.gemm_rms_norm_workspace_size.argtypes = [i64, i64]
+    lib.gemm_rms_norm_workspace_size.restype = i64
+    lib.gemm_rms_norm_backward.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, vp, i64, vp]
+    lib.gemm_block_scaled.argtypes = [i32, i64, i64, i64, f32, vp, i64, vp, i64, scales, i32, vp, i64, vp]
+    lib.gemm_grouped.argtypes = [i32, i32, i32, vp, i64, i64, i64, f32, vp, i64, vp, i64, i64, scales, i32, vp, i64,
+                                 vp]
+    lib.gemm_grouped_wgrad.argtypes = [i32, i32, vp, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, i64, vp]
+    for fn in (lib.gemm_quantize, lib.gemm_rms_norm, lib.gemm_rms_norm_backward, lib.gemm_block_scaled,
+               lib.gemm_grouped, lib.gemm_grouped_wgrad):
+        fn.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -288,3 +311,39 @@ def gemm_tuning_save(path: str) -> int:
 
 def gemm_tuning_load(path: str) -> int:
     return int(load().gemm_tuning_load(path.encode()))
+
+
+def gemm_quantize(dtype, block_rows, M, K, X, ldx, Q, ldq, scales, lds, stream=0) -> int:
+    return load().gemm_quantize(dtype, block_rows, M, K, X, ldx, Q, ldq, scales, lds, stream)
+
+
+def gemm_rms_norm(dtype, M, N, X, ldx, residual, ldr, weight, eps, sum, ld_sum, out_type, out, ldo, scales=0,
+                  ld_scales=0, stream=0) -> int:
+    return load().gemm_rms_norm(dtype, M, N, X, ldx, residual, ldr, weight, eps, sum, ld_sum, out_type, out, ldo,
+                                scales, ld_scales, stream)
+
+
+def gemm_rms_norm_workspace_size(M, N) -> int:
+    return int(load().gemm_rms_norm_workspace_size(M, N))
+
+
+def gemm_rms_norm_backward(dtype, M, N, dY, lddy, S, lds, weight, eps, dS, ldds, dX, lddx, dweight=0, workspace=0,
+                           workspace_bytes=0, stream=0) -> int:
+    return load().gemm_rms_norm_backward(dtype, M, N, dY, lddy, S, lds, weight, eps, dS, ldds, dX, lddx, dweight,
+                                         workspace, workspace_bytes, stream)
+
+
+def gemm_block_scaled(op_b, M, N, K, alpha, A, lda, B, ldb, scales, out_type, out, ldo, stream=0) -> int:
+    return load().gemm_block_scaled(op_b, M, N, K, alpha, A, lda, B, ldb, scales, out_type, out, ldo, stream)
+
+
+def gemm_grouped(dtype, op_b, groups, ends, M, N, K, alpha, A, lda, B, ldb, stride_b, scales, out_type, out, ldo,
+                 stream=0) -> int:
+    return load().gemm_grouped(dtype, op_b, groups, ends, M, N, K, alpha, A, lda, B, ldb, stride_b, scales, out_type,
+                               out, ldo, stream)
+
+
+def gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w,
+                       stream=0) -> int:
+    return load().gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w,
+                                     stream)

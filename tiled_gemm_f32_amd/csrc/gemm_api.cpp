@@ -21,6 +21,27 @@
 #include "gemm.h"
 #include "gemm_kernels.hpp"
 
+namespace gemm {
+
+// The current device must be a gfx950; checked once per device and cached.
+static std::atomic<int8_t> g_device_ok[64];
+
+gemm_status check_device() {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GEMM_ERR_DEVICE;
+    if (dev < 64) {
+        const int8_t known = g_device_ok[dev].load(std::memory_order_relaxed);
+        if (known != 0) return known > 0 ? GEMM_OK : GEMM_ERR_DEVICE;
+    }
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_ERR_DEVICE;
+    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    if (dev < 64) g_device_ok[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
+    return ok ? GEMM_OK : GEMM_ERR_DEVICE;
+}
+
+}  // namespace gemm
+
 namespace {
 
 using gemm::KernelDesc;
@@ -573,22 +594,7 @@ gemm_status plan(const Call &c, int32_t force, gemm_plan *out, const KernelDesc 
     return GEMM_OK;
 }
 
-// The current device must be a gfx950; checked once per device and cached.
-std::atomic<int8_t> g_device_ok[64];
-
-gemm_status check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GEMM_ERR_DEVICE;
-    if (dev < 64) {
-        const int8_t known = g_device_ok[dev].load(std::memory_order_relaxed);
-        if (known != 0) return known > 0 ? GEMM_OK : GEMM_ERR_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_ERR_DEVICE;
-    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 64) g_device_ok[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
-    return ok ? GEMM_OK : GEMM_ERR_DEVICE;
-}
+using gemm::check_device;
 
 gemm_status launch(const Call &c, const gemm_plan &pl, const KernelDesc *kd, const KSplit &ks, hipStream_t s);
 

@@ -1,0 +1,151 @@
+// Shared by the grouped and block-scaled products (gemm_grouped, gemm_block_scaled,
+// gemm_grouped_wgrad): their arguments, and the map from a workgroup to a tile
+// of a group.
+//
+// The rows of A are sorted by group and only the device knows where groups
+// end.  A launch therefore covers the most row tiles that any division of M
+// rows can need, and each workgroup finds its tile itself: every wave reads
+// the ends 64 at a time, turns them into tile counts, and scans those across
+// its lanes.  Workgroups past the real count leave at once.
+#pragma once
+
+#include "gemm_device.hpp"
+
+namespace gemm {
+
+// One launch, already validated (gemm_experts_api.cpp): sizes below 2^31,
+// pointers aligned to their elements.
+struct GroupedParams {
+    const void *A;
+    const void *B;
+    void *out;
+    const int32_t *ends;       // null: one group of all M rows
+    int32_t M, N, K, groups;
+    int64_t lda, ldb, stride_b, ldo;
+    int64_t stride_out;        // weight gradients: elements between groups' results
+    float alpha, beta;         // beta: weight gradients only
+    int32_t out_type;          // GEMM_OUT_F32 or GEMM_OUT_BF16
+    gemm_block_scales sc;      // fp8 only
+};
+
+// Most row tiles of `tile_m` rows that M rows in `groups` groups can make,
+// the rows past the last end counted as one group more: each of c groups
+// that have rows adds at most one tile to the M / tile_m whole ones.
+inline int64_t most_row_tiles(int64_t M, int64_t groups, int64_t tile_m, bool grouped) {
+    if (!grouped) return (M + tile_m - 1) / tile_m;
+    const int64_t c = groups + 1 < M ? groups + 1 : M;
+    return c + (M - c) / tile_m;
+}
+
+#if defined(__HIPCC__)
+
+// A tile's rows: `rows` of them from row0; group is -1 for the rows past the
+// last end, which are zeroed; rows == 0: nothing to do.  tn: tile column.
+struct GroupTile {
+    int group, row0, rows, tn;
+};
+
+// Inclusive scans over the 64 lanes.
+__device__ __forceinline__ int wave_scan_max(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v = max(v, o);
+    }
+    return v;
+}
+__device__ __forceinline__ int wave_scan_add(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// First row and past-the-last row of group `lane + 64 * chunk` (the group
+// after the last one: the rows past every end), from the ends clamped to
+// their running maximum and to M.  `carry` is the running maximum of the
+// chunks before and is moved on.
+__device__ __forceinline__ void group_bounds(const GroupedParams &p, int chunk, int lane, int &carry, int &lo,
+                                             int &hi) {
+    const int g = 64 * chunk + lane;
+    int e = g < p.groups ? min(max(p.ends[g], 0), p.M) : g == p.groups ? p.M : 0;
+    e = max(wave_scan_max(e, lane), carry);
+    const int before = __shfl_up(e, 1);
+    lo = lane == 0 ? carry : before;
+    hi = e;
+    carry = __shfl(e, 63);
+}
+
+// The tile of workgroup `wg`, for tiles of tile_m rows and tiles_n columns of
+// tiles.  Tiles are walked in the order of tile_coords over the real number
+// of row tiles, so the dead workgroups of the launch are its last ones.
+__device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, int tile_m, int tiles_n, int group_m) {
+    GroupTile t;
+    if (p.ends == nullptr) {
+        int tm;
+        tile_coords(wg, (p.M + tile_m - 1) / tile_m, tiles_n, group_m, tm, t.tn);
+        t.group = 0;
+        t.row0 = tm * tile_m;
+        t.rows = min(tile_m, p.M - t.row0);
+        return t;
+    }
+    const int lane = threadIdx.x & 63;
+    const int chunks = p.groups / 64 + 1;
+    int carry = 0, total = 0, lo, hi, upto = 0, mine = 0;
+    for (int c = 0; c < chunks; ++c) {
+        group_bounds(p, c, lane, carry, lo, hi);
+        mine = (hi - lo + tile_m - 1) / tile_m;
+        upto = wave_scan_add(mine, lane) + total;
+        total = __shfl(upto, 63);
+    }
+    t.group = 0;
+    t.row0 = t.rows = t.tn = 0;
+    if ((int64_t)wg >= (int64_t)total * tiles_n) return t;
+    int tm;
+    tile_coords(wg, total, tiles_n, group_m, tm, t.tn);
+    int last = chunks - 1;
+    if (chunks > 1) {         // find the chunk of 64 groups again that holds tile tm
+        carry = 0;
+        total = 0;
+        for (last = 0; last < chunks; ++last) {
+            group_bounds(p, last, lane, carry, lo, hi);
+            mine = (hi - lo + tile_m - 1) / tile_m;
+            upto = wave_scan_add(mine, lane) + total;
+            total = __shfl(upto, 63);
+            if (tm < total) break;
+        }
+    }
+    const int src = __ffsll((unsigned long long)__ballot(upto > tm)) - 1;
+    const int first = __shfl(upto - mine, src), row = __shfl(lo, src), end = __shfl(hi, src);
+    const int g = 64 * last + src;
+    t.group = g < p.groups ? g : -1;
+    t.row0 = row + (tm - first) * tile_m;
+    t.rows = min(tile_m, end - t.row0);
+    // The same in every lane: tell the compiler, so that addresses made of it are scalar.
+    t.group = __builtin_amdgcn_readfirstlane(t.group);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    return t;
+}
+
+// Rows [lo, hi) of group g (weight gradients: one group a workgroup).
+__device__ __forceinline__ void find_group(const GroupedParams &p, int g, int &lo, int &hi) {
+    const int lane = threadIdx.x & 63;
+    int carry = 0;
+    for (int c = 0;; ++c) {
+        group_bounds(p, c, lane, carry, lo, hi);
+        if (g < 64 * (c + 1)) break;
+    }
+    lo = __builtin_amdgcn_readfirstlane(__shfl(lo, g & 63));
+    hi = __builtin_amdgcn_readfirstlane(__shfl(hi, g & 63));
+}
+
+#endif  // __HIPCC__
+
+// Launchers.  The general ones run every type, layout and alignment.
+hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_wgrad_general(int32_t dtype, const GroupedParams &p, hipStream_t stream);
+
+}  // namespace gemm

@@ -126,6 +126,9 @@ constexpr int64_t kStaticScratchBytes = int64_t(32) << 20;
 // once per device).
 hipError_t static_scratch(void **ptr);
 
+// GEMM_OK when the current device is a gfx950 (gemm_api.cpp).
+gemm_status check_device();
+
 // The K == 0 / alpha == 0 result over p's M x N view: act(beta * C + bias)
 // (C not read when beta == 0), stored as p's output type.
 hipError_t launch_scale_c(const GemmParams &p, hipStream_t stream);
