@@ -25,6 +25,10 @@ bool bad_opt(const void *p, uintptr_t esz) { return p != nullptr && !aligned(p, 
 bool float_type(int32_t dtype) { return dtype == GEMM_DTYPE_F32 || dtype == GEMM_DTYPE_BF16F32; }
 uintptr_t size_of(int32_t dtype) { return dtype == GEMM_DTYPE_F32 ? 4 : dtype == GEMM_DTYPE_BF16F32 ? 2 : 1; }
 
+bool rows_on16(const void *p, int64_t ld, int64_t esz) { return aligned(p, 16) && ld * esz % 16 == 0; }
+// Offsets inside a tile's panel of 256 rows (and of their scales) are 32-bit.
+constexpr int64_t kMaxTileRow = (int64_t(1) << 31) / 256 - 256;
+
 gemm_status launched(hipError_t err) { return err == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 struct Product {
@@ -89,7 +93,16 @@ gemm_status run(const Product &c, gemm_stream_t stream) {
     p.alpha = c.alpha;
     p.out_type = c.out_type;
     if (c.sc != nullptr) p.sc = *c.sc;
-    return launched(gemm::launch_grouped_general(c.dtype, c.op_b, p, static_cast<hipStream_t>(stream)));
+    // A row's bytes must hold one 16-byte load, whatever their alignment.
+    const int64_t sz = (int64_t)esz;
+    const bool tiles = c.dtype != GEMM_DTYPE_F32 && c.K * sz >= 16 && b_len * sz >= 16 && c.lda * sz < kMaxTileRow &&
+                       c.ldb * sz < kMaxTileRow && (c.sc == nullptr || c.sc->a_row * 4 < kMaxTileRow);
+    const auto s = static_cast<hipStream_t>(stream);
+    if (!tiles) return launched(gemm::launch_grouped_general(c.dtype, c.op_b, p, s));
+    if (c.M == 1) p.lda = ceil_div(c.K * sz, 16) * 16 / sz;          // the stride of a single row is not used
+    const bool dma = rows_on16(c.A, p.lda, sz) && rows_on16(c.B, c.ldb, sz) && c.stride_b * sz % 16 == 0;
+    return launched(c.dtype == GEMM_DTYPE_FP8F32 ? gemm::launch_grouped_fp8(c.op_b, dma, p, s)
+                                                 : gemm::launch_grouped_bf16(c.op_b, dma, p, s));
 }
 
 }  // namespace
@@ -149,7 +162,11 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
     p.stride_out = stride_w;
     p.alpha = alpha;
     p.beta = beta;
-    return launched(gemm::launch_wgrad_general(dtype, p, static_cast<hipStream_t>(stream)));
+    const int64_t sz = (int64_t)esz;
+    const auto s = static_cast<hipStream_t>(stream);
+    if (dtype == GEMM_DTYPE_F32 || N * sz < 16 || K * sz < 16 || lddy * sz >= kMaxTileRow || ldx * sz >= kMaxTileRow)
+        return launched(gemm::launch_wgrad_general(dtype, p, s));
+    return launched(gemm::launch_wgrad_bf16(rows_on16(dY, lddy, sz) && rows_on16(X, ldx, sz), p, s));
 }
 
 GEMM_API gemm_status gemm_quantize(int32_t dtype, int32_t block_rows, int64_t M, int64_t K, const void *X, int64_t ldx,

@@ -98,7 +98,7 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, i
         group_bounds(p, c, lane, carry, lo, hi);
         mine = (hi - lo + tile_m - 1) / tile_m;
         upto = wave_scan_add(mine, lane) + total;
-        total = __shfl(upto, 63);
+        total = __builtin_amdgcn_readlane(upto, 63);      // scalar, so that no lane seems to differ
     }
     t.group = 0;
     t.row0 = t.rows = t.tn = 0;
@@ -113,20 +113,16 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, i
             group_bounds(p, last, lane, carry, lo, hi);
             mine = (hi - lo + tile_m - 1) / tile_m;
             upto = wave_scan_add(mine, lane) + total;
-            total = __shfl(upto, 63);
+            total = __builtin_amdgcn_readlane(upto, 63);
             if (tm < total) break;
         }
     }
-    const int src = __ffsll((unsigned long long)__ballot(upto > tm)) - 1;
+    const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(upto > tm)) - 1);
     const int first = __shfl(upto - mine, src), row = __shfl(lo, src), end = __shfl(hi, src);
     const int g = 64 * last + src;
     t.group = g < p.groups ? g : -1;
     t.row0 = row + (tm - first) * tile_m;
     t.rows = min(tile_m, end - t.row0);
-    // The same in every lane: tell the compiler, so that addresses made of it are scalar.
-    t.group = __builtin_amdgcn_readfirstlane(t.group);
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
     return t;
 }
 
@@ -144,7 +140,12 @@ __device__ __forceinline__ void find_group(const GroupedParams &p, int g, int &l
 
 #endif  // __HIPCC__
 
-// Launchers.  The general ones run every type, layout and alignment.
+// Launchers.  The general ones run every type, layout and alignment; the
+// others the tiles of gemm_grouped_tile.hpp.  dma: rows of both operands
+// start on 16 bytes.
+hipError_t launch_grouped_fp8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_grouped_bf16(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_wgrad_bf16(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_general(int32_t dtype, const GroupedParams &p, hipStream_t stream);
 

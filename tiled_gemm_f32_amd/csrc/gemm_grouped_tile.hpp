@@ -1,0 +1,540 @@
+// Tile kernel of the grouped and block-scaled products, for bf16 and fp8
+// operands: instantiated in gemm_grouped_bf16.hip and gemm_grouped_fp8.hip.
+//
+// A workgroup makes a tile of BM x BN outputs of one group, walking k in
+// slabs of 128 bytes a row (64 bf16 or 128 fp8 values: for fp8 exactly one
+// scale block).  Two LDS stages of a slab each: while a slab is multiplied
+// the next one lands in the other stage.  WM x WN waves each hold 32*FM x
+// 32*FN outputs; a wave keeps the slab's B fragments and two sets of A
+// fragments in registers, so every LDS byte of A is read once a wave and the
+// reads of A fragment i + 1 (or of the next slab) run under the products of
+// fragment i.
+//
+// fp8 with block scales: the matrix core sums a block of 128 k into a partial
+// tile of its own (two v_mfma_f32_32x32x64_f8f6f4, the first with a zero
+// addend), which is then added to the accumulators times the block's scale,
+// a(row) * b(column block): 16 fused multiply-adds a fragment (64 cycles)
+// beside 128 matrix cycles, issued while the other wave of the SIMD has the
+// matrix core.  The accumulators must be architectural registers for that,
+// which is why a wave's tile is 128 x 64 and two waves share a SIMD (the
+// 128 x 128 wave tile of the per-tensor fp8 kernels fills the accumulation
+// registers, which only matrix instructions can add to).
+//
+// LDS layouts, in 16-byte chunks:
+//   k-contiguous operand: [rows][8 chunks]; chunk c of row r at
+//     c ^ ((r >> 1) & 7): 32 rows at one chunk touch every bank group of the
+//     256-byte period twice a half-wave.
+//   bf16 stored the other way: [64-column block][64 k][8 chunks], chunk c of
+//     k row r at c ^ 4*((r >> 1) & 1), read with ds_read_b64_tr_b16.
+//   fp8 stored the other way: [128-column block][128 k][8 chunks], chunk c of
+//     k row r at c ^ (r & 7), read with ds_read_b64_tr_b8.
+//
+// DMA: operands whose rows start on 16 bytes come by direct-to-LDS buffer
+// loads.  Rows and k past the ends fall outside the buffer resource (or get
+// an offset that does) and read as zero; a 16-byte chunk that straddles the
+// end of K is cut in LDS before it is read.  Otherwise (REG) chunks go
+// through registers with unaligned 16-byte loads, the last one of a row
+// loaded so that it ends with the row and shifted into place.
+#pragma once
+
+#include "gemm_grouped.hpp"
+
+#if defined(__HIPCC__)
+
+namespace gemm {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+typedef unsigned __int128 u128;
+
+constexpr int kSlab = 128;              // bytes of k a slab holds of every row
+
+// 16 bytes at any alignment of their elements.
+struct __attribute__((packed, aligned(1))) Bytes16 {
+    u32x4 v;
+};
+
+template <int DT_, int FM_, int FN_, int WM_, int WN_, bool AKN_, bool BKN_, bool DMA_>
+struct TileConfig {
+    static constexpr int DT = DT_, FM = FM_, FN = FN_, WM = WM_, WN = WN_;
+    static constexpr bool AKN = AKN_, BKN = BKN_, DMA = DMA_;
+    static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
+    static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : 2;
+    static constexpr int BK = kSlab / esz;            // k a slab
+    static constexpr int kA = BM * kSlab, kB = BN * kSlab, kStage = kA + kB;
+};
+
+// One operand of a tile as the loads see it: KN false: `rows` rows of
+// `len` k at base (row stride ld); KN true: `len` rows of k, `rows` columns.
+template <class C, bool KN, int ROWS>
+struct Loader {
+    static constexpr int esz = C::esz;
+    static constexpr int kLoads = ROWS * 8 / (64 * C::NW);    // 16-byte chunks a thread and slab
+    static constexpr int kGroups = C::BK / 8;                 // KN: groups of 8 k rows a slab
+    const char *base;
+    int64_t ld;          // bytes
+    int rows, len;       // elements
+    uint32_t off;        // this lane's offset in load 0
+    int chunk;           // byte of the row (k or columns) this lane's chunk starts at
+    u32x4 reg[C::DMA ? 1 : kLoads];
+
+    __device__ __forceinline__ void init(int wave, int lane) {
+        const int r = 8 * wave + (lane >> 3);
+        const int swz = !KN ? (r >> 1) & 7 : esz == 2 ? 4 * ((r >> 1) & 1) : r & 7;
+        chunk = 16 * ((lane & 7) ^ swz);
+        off = (uint32_t)(r * (int)ld + chunk);
+    }
+    // First row (KN: k row) and first byte along the row of load j, over all waves.
+    static __device__ __forceinline__ constexpr int row_of(int j) {
+        return KN ? 8 * ((j * C::NW) % kGroups) : 8 * C::NW * j;
+    }
+    static __device__ __forceinline__ constexpr int byte_of(int j) { return KN ? kSlab * ((j * C::NW) / kGroups) : 0; }
+
+    // Slab t into `stage` (DMA) or into the staging registers.
+    __device__ __forceinline__ void fetch(int t, char *stage, int wave, int lane) {
+        if constexpr (C::DMA) {
+            // Bounds in 32 bits and without branches, which would cut the loop's schedule: a
+            // panel of 256 rows is below 2^31 bytes (checked on the host).
+            const int step = (int)ld;
+            const int left = KN ? len - t * C::BK : len * esz - t * kSlab;          // KN: rows, else bytes
+            const char *src = base + (KN ? (int64_t)t * C::BK * ld : (int64_t)t * kSlab);
+            const int wide = ((KN ? rows * esz : max(left, 0)) + 15) & ~15;         // whole chunks
+            const int deep = KN ? min(left, C::BK) : rows;
+            const rsrc_t rs = make_rsrc(src, (uint32_t)max(deep * step - (step - wide), 0));
+            uint32_t at = off;
+            if (!KN) at += (uint32_t)(chunk >= left) << 31;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
+                                                         at + (uint32_t)(row_of(j) * step + byte_of(j)), 0, 0, 0);
+        } else {
+            const int64_t k0 = (int64_t)t * C::BK;
+            const int r0 = 8 * wave + (lane >> 3);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int64_t r = row_of(j) + r0;
+                const int64_t b = byte_of(j) + chunk;
+                const int64_t row = KN ? k0 + r : r, last = KN ? len - 1 : rows - 1;
+                const int64_t byte = KN ? b : b + k0 * esz, wide = (int64_t)(KN ? rows : len) * esz;
+                const int64_t from = byte < wide - 16 ? byte : wide - 16;
+                const char *src = base + (row < last ? row : last) * ld + from;
+                u32x4 v = reinterpret_cast<const Bytes16 *>(src)->v;
+                if ((KN ? byte_of(j) : k0 * esz) + kSlab > wide) {          // a slab that holds the row's end
+                    const int64_t shift = byte - from;
+                    const u128 w = shift < 16 ? __builtin_bit_cast(u128, v) >> (8 * (int)shift) : (u128)0;
+                    v = __builtin_bit_cast(u32x4, w);
+                }
+                if (KN && row > last) v = u32x4{};
+                reg[j] = v;
+            }
+        }
+    }
+    __device__ __forceinline__ void stash(char *stage, int wave, int lane) const {
+        if constexpr (!C::DMA) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                *reinterpret_cast<u32x4 *>(stage + (j * C::NW + wave) * 1024 + lane * 16) = reg[j];
+        }
+    }
+    // Zero the bytes past K of the chunk that straddles it, in every row of the slab that ends K.
+    __device__ __forceinline__ void cut(char *stage, int tail_bytes) const {
+        if constexpr (!KN) {
+            for (int r = threadIdx.x; r < ROWS; r += 64 * C::NW) {
+                uint32_t *at = reinterpret_cast<uint32_t *>(stage + r * kSlab + 16 * ((tail_bytes >> 4) ^ ((r >> 1) & 7)));
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int n = (tail_bytes & 15) - 4 * d;         // valid bytes from here on
+                    const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+                    at[d] &= keep;
+                }
+            }
+        }
+    }
+};
+
+// One 32-row fragment of a slab: 16 registers a lane, grouped as the matrix
+// instruction takes them (fp8: two of 64 k; bf16: four of 16 k), so that they
+// are read into place.
+template <int ESZ> struct FragOf {
+    u32x4 q[4];
+};
+template <> struct FragOf<1> {
+    i32x8 h[2];
+};
+
+// Offset in a panel of this lane's first read of the fragment at row (column) 32 * f.
+template <class C, bool KN> __device__ __forceinline__ uint32_t frag_base(int f, int lane) {
+    const int h = lane >> 5, l32 = lane & 31;
+    if constexpr (!KN) {
+        const int c = C::esz == 1 ? 2 * h : h;
+        return (uint32_t)((32 * f + l32) * kSlab + 16 * (c ^ ((l32 >> 1) & 7)));
+    } else if constexpr (C::esz == 2) {
+        const int q = lane >> 4, j16 = lane & 15;
+        const int row = 8 * (q >> 1) + (j16 >> 2);
+        const int c = 2 * (q & 1) + ((j16 & 3) >> 1) + 4 * ((f & 1) ^ ((row >> 1) & 1));
+        return (uint32_t)((f >> 1) * (C::BK * kSlab) + row * kSlab + 16 * c + 8 * (j16 & 1));
+    } else {
+        const int s16 = lane & 15;
+        const int e = ((s16 >> 1) & 3) + 4 * (s16 >> 3);
+        const int c = (2 * f + (l32 >> 4)) & 7;
+        return (uint32_t)((f >> 2) * (C::BK * kSlab) + (32 * h + e) * kSlab + 16 * (c ^ e) + 8 * (s16 & 1));
+    }
+}
+// Fragment i after the one `base` is for (a multiple of the wave's number of
+// them), all 128 bytes of k.  Further chunks are the first one's offset with
+// bits flipped, the swizzles being exclusive ors.
+template <class C, bool KN>
+__device__ __forceinline__ FragOf<C::esz> read_frag(const char *panel, uint32_t base, int i) {
+    FragOf<C::esz> v;
+    if constexpr (!KN) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            // fp8: 32 consecutive bytes of each half; bf16: 16 bytes of each 32.
+            const uint32_t flip = 16u * (C::esz == 1 ? 4 * (q >> 1) + (q & 1) : 2 * q);
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(panel + ((base ^ flip) + 32 * kSlab * i));
+            if constexpr (C::esz == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v.h[q >> 1][4 * (q & 1) + e] = (int)w[e];
+            } else {
+                v.q[q] = w;
+            }
+        }
+    } else if constexpr (C::esz == 2) {
+        const char *at = panel + ((base ^ (64u * (i & 1))) + (i >> 1) * (C::BK * kSlab));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 16 * kSlab * q));
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 16 * kSlab * q + 4 * kSlab));
+            v.q[q] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    } else {
+        const char *at = panel + (base ^ (32u * i));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + (64 * (q >> 2) + 8 * (q & 3)) * kSlab));
+            v.h[q >> 2][2 * (q & 3)] = w[0];
+            v.h[q >> 2][2 * (q & 3) + 1] = w[1];
+        }
+    }
+    return v;
+}
+
+// B^T as the first operand and A^T as the second: register 4g + t of lane
+// (h, l32) is row l32, column 8g + 4h + t of the fragment.
+__device__ __forceinline__ f32x16 product_fp8(const FragOf<1> &a, const FragOf<1> &b) {
+    f32x16 part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.h[0], a.h[0], f32x16{}, 0, 0, 0, 0,
+                                                                   0, 0);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.h[1], a.h[1], part, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 product_bf16(const FragOf<2> &a, const FragOf<2> &b, f32x16 acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b.q[i]),
+                                                      __builtin_bit_cast(bf16x8, a.q[i]), acc, 0, 0, 0);
+    return acc;
+}
+
+template <class C>
+__global__ void __launch_bounds__(64 * C::NW, 2)
+grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
+    constexpr int FM = C::FM, FN = C::FN, NW = C::NW, BM = C::BM, BN = C::BN;
+    constexpr bool FP8 = C::DT == GEMM_DTYPE_FP8F32, WGRAD = C::AKN;
+    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+
+    Loader<C, C::AKN, BM> a;
+    Loader<C, C::BKN, BN> b;
+    int group, row0, n0, out_rows, out_cols;
+    int64_t out_at;
+    const char *A = static_cast<const char *>(p.A), *B = static_cast<const char *>(p.B);
+    if (WGRAD) {
+        int tm, tn, lo, hi;
+        tile_coords(blockIdx.x, tiles_m, tiles_n, 4, tm, tn);
+        group = blockIdx.y;
+        find_group(p, group, lo, hi);
+        row0 = __builtin_amdgcn_readfirstlane(tm) * BM;
+        n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
+        a.base = A + ((int64_t)lo * p.lda + row0) * C::esz;
+        b.base = B + ((int64_t)lo * p.ldb + n0) * C::esz;
+        a.rows = out_rows = min(BM, p.N - row0);
+        b.rows = out_cols = min(BN, p.K - n0);
+        a.len = b.len = hi - lo;
+        out_at = (int64_t)group * p.stride_out + (int64_t)row0 * p.ldo + n0;
+    } else {
+        GroupTile t = find_tile(p, blockIdx.x, BM, tiles_n, 4);
+        // Integer divisions are vector code: make their results scalar again, so that the
+        // buffer resources below are.
+        t.group = __builtin_amdgcn_readfirstlane(t.group);
+        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+        t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+        if (t.rows <= 0) return;
+        group = max(t.group, 0);
+        row0 = t.row0;
+        n0 = t.tn * BN;
+        a.base = A + (int64_t)row0 * p.lda * C::esz;
+        b.base = B + ((int64_t)group * p.stride_b + (C::BKN ? (int64_t)n0 : (int64_t)n0 * p.ldb)) * C::esz;
+        a.rows = out_rows = t.rows;
+        b.rows = out_cols = min(BN, p.N - n0);
+        a.len = b.len = t.group < 0 ? 0 : p.K;
+        out_at = (int64_t)row0 * p.ldo + n0;
+    }
+    a.ld = p.lda * C::esz;
+    b.ld = p.ldb * C::esz;
+    a.init(wave, lane);
+    b.init(wave, lane);
+
+    // Slabs that are read as they land; with a chunk across K one more, cut first.
+    const int len = a.len;
+    const bool cut = C::DMA && (!C::AKN || !C::BKN) && (int64_t)len * C::esz % 16 != 0;
+    const int nk = cut ? len / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
+
+    const int l32 = lane & 31;
+    // Scales of the block that slab t is: a's of this lane's rows, b's of the wave's columns.
+    const float *sa = nullptr, *sb = nullptr;
+    uint32_t sa_off[FM];
+    float sc_a[2][FM], sc_b[2];
+    if (FP8) {
+        const int col0 = n0 + wn * 32 * FN;
+        sa = p.sc.a + (int64_t)row0 * p.sc.a_row;
+        sb = p.sc.b + (int64_t)group * p.sc.b_group + (int64_t)(col0 < p.N ? col0 / GEMM_SCALE_BLOCK : 0) * p.sc.b_n;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            sa_off[i] = (uint32_t)min((wm * FM + i) * 32 + l32, out_rows - 1) * (uint32_t)p.sc.a_row * 4u;
+    }
+    const int blocks = (int)(((int64_t)len + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK);
+    auto scales = [&](int t, int set) __attribute__((always_inline)) {
+        if constexpr (FP8) {
+            const int k = min(t, blocks - 1);
+            sc_b[set] = sb[k * p.sc.b_k];
+            const rsrc_t col = make_rsrc(sa + k * p.sc.a_block, (uint32_t)((out_rows - 1) * (int)p.sc.a_row + 1) * 4u);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sc_a[set][i] = __builtin_bit_cast(float, load_b32(col, sa_off[i]));
+        }
+    };
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    FragOf<C::esz> fa[2], fb[FN];
+    static_assert(FM <= 2 || !C::AKN || C::esz == 2, "");
+    uint32_t a_base = frag_base<C, C::AKN>(wm * FM, lane), b_base = frag_base<C, C::BKN>(wn * FN, lane);
+    auto read_a = [&](const char *st, int i) { return read_frag<C, C::AKN>(st, a_base, i); };
+    auto read_b = [&](const char *st, int j) { return read_frag<C, C::BKN>(st + C::kA, b_base, j); };
+    auto fetch = [&](int t, char *st) {
+        a.fetch(t, st, wave, lane);
+        b.fetch(t, st + C::kA, wave, lane);
+    };
+    auto stash = [&](char *st) {
+        a.stash(st, wave, lane);
+        b.stash(st + C::kA, wave, lane);
+    };
+
+    // Products of slab t, whose fragments (B's, and A's first) are in
+    // registers, from stage `cur`; meanwhile slab t + 1 lands in `next`, whose
+    // first fragments are read at the end, and slab t + 2 is sent for.
+    // `first`: the set that holds A's first fragment; `set`: that of the scales.
+    auto slab = [&](int t, char *cur, char *next, int first, int set) __attribute__((always_inline)) {
+        // Addresses are made again from these in every slab: kept across the loop they would
+        // take more registers than there are.
+        asm volatile("" : "+v"(a_base), "+v"(b_base), "+v"(a.off), "+v"(b.off));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int s = (first + i) & 1;
+            if (i + 1 < FM) {
+                fa[s ^ 1] = read_a(cur, i + 1);
+            } else {
+                stash(next);
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+                __builtin_amdgcn_s_barrier();
+                fa[s ^ 1] = read_a(next, 0);
+                fetch(t + 2, cur);
+            }
+            const float s_ab = FP8 ? sc_a[set][i] * sc_b[set] : 0.0f;
+            // A partial tile is added while the next one is multiplied; with 128
+            // accumulators there are registers for one only, and the SIMD's
+            // other wave has the matrix core meanwhile.
+            constexpr int kParts = FM * FN >= 99 ? 1 : FN;
+            f32x16 part[kParts];
+            auto add = [&](int j) __attribute__((always_inline)) {
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(part[j % kParts][e], s_ab, acc[i][j][e]);
+                }
+            };
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (FP8) part[j % kParts] = product_fp8(fa[s], fb[j]);
+                else acc[i][j] = product_bf16(fa[s], fb[j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + 1 == FM) fb[j] = read_b(next, j);
+                if (kParts == 1 && FN > 1) add(j);
+                else if (j > 0) add(j - 1);
+            }
+            if (kParts > 1 || FN == 1) add(FN - 1);
+            if (i + 1 == FM) scales(t + 2, set);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    if (len > 0) {
+        scales(0, 0);
+        scales(1, 1);
+        fetch(0, st0);
+        stash(st0);
+        fetch(1, st1);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(C::DMA ? a.kLoads + b.kLoads : 63));
+        __builtin_amdgcn_s_barrier();
+        fa[0] = read_a(st0, 0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = read_b(st0, j);
+        int t = 0;
+        for (; t + 1 < nk; t += 2) {
+            slab(t, st0, st1, 0, 0);
+            slab(t + 1, st1, st0, FM & 1, 1);
+        }
+        if (t < nk) slab(t, st0, st1, 0, 0);
+        if (cut) {
+            // Slab nk ends K inside a chunk.  It has landed (slab 0: the wait above), every
+            // wave has read what it will of it, and it is read again.
+            char *cur = (nk & 1) ? st1 : st0, *next = (nk & 1) ? st0 : st1;
+            const int tail = (int)(((int64_t)len - (int64_t)nk * C::BK) * C::esz);
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+            __builtin_amdgcn_s_barrier();
+            a.cut(cur, tail);
+            b.cut(cur + C::kA, tail);
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+            __builtin_amdgcn_s_barrier();
+            fa[0] = read_a(cur, 0);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) fb[j] = read_b(cur, j);
+            if (nk & 1) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i) sc_a[0][i] = sc_a[1][i];
+                sc_b[0] = sc_b[1];
+            }
+            slab(nk, cur, next, 0, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+        __builtin_amdgcn_s_barrier();
+    }
+
+    // Epilogue: 32 rows of the wave's columns at a time through its own piece
+    // of LDS, so that a store instruction writes whole runs of a row.
+    constexpr int kPiece = 32 * FN * 128, kFit = C::kStage / kPiece;
+    constexpr int kChunks = 8 * FN;                  // 16-byte chunks (4 columns) of a row
+    char *piece = wave < kFit ? st0 + wave * kPiece : st1 + (wave - kFit) * kPiece;
+    float *of = static_cast<float *>(p.out) + out_at;
+    uint16_t *oh = static_cast<uint16_t *>(p.out) + out_at;
+    const bool bf16_out = !WGRAD && p.out_type == GEMM_OUT_BF16;
+    const uintptr_t at = bf16_out ? reinterpret_cast<uintptr_t>(oh) & 7 : reinterpret_cast<uintptr_t>(of) & 15;
+    const bool vec = at == 0 && p.ldo % 4 == 0;
+    const int cc = lane % kChunks;
+    const int col = wn * 32 * FN + 4 * cc;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = (8 * j + 2 * g + (lane >> 5)) ^ (l32 & (kChunks - 1));
+                *reinterpret_cast<f32x4 *>(piece + l32 * (kChunks * 16) + 16 * c) =
+                    f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            }
+        constexpr int kRows = 64 / kChunks;          // rows an instruction takes
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kRows) {
+            const int r = r0 + lane / kChunks;
+            f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (kChunks * 16) + 16 * (cc ^ (r & (kChunks - 1))));
+            const int row = (wm * FM + i) * 32 + r;
+            if (row >= out_rows || col >= out_cols) continue;
+            const int64_t o = (int64_t)row * p.ldo + col;
+            const bool whole = col + 4 <= out_cols;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
+            if (bf16_out) {
+                const uint32_t h0 = to_bf16(v[0]), h1 = to_bf16(v[1]), h2 = to_bf16(v[2]), h3 = to_bf16(v[3]);
+                if (vec && whole) {
+                    *reinterpret_cast<u32x2 *>(oh + o) = u32x2{h0 | (h1 << 16), h2 | (h3 << 16)};
+                } else {
+                    const uint32_t hs[4] = {h0, h1, h2, h3};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < out_cols) oh[o + e] = (uint16_t)hs[e];
+                }
+            } else {
+                if (WGRAD && p.beta != 0.0f) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < out_cols) v[e] = fmaf(p.beta, of[o + e], v[e]);
+                }
+                if (vec && whole) {
+                    *reinterpret_cast<f32x4 *>(of + o) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < out_cols) of[o + e] = v[e];
+                }
+            }
+        }
+    }
+}
+
+template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStream_t stream) {
+    GroupedParams args = p;
+    int tiles_m, tiles_n;
+    dim3 grid;
+    if (C::AKN) {
+        tiles_m = (p.N + C::BM - 1) / C::BM;
+        tiles_n = (p.K + C::BN - 1) / C::BN;
+        grid = dim3((unsigned)(tiles_m * tiles_n), (unsigned)p.groups);
+    } else {
+        tiles_m = (int)most_row_tiles(p.M, p.groups, C::BM, p.ends != nullptr);
+        tiles_n = (p.N + C::BN - 1) / C::BN;
+        grid = dim3((unsigned)(tiles_m * tiles_n));
+    }
+    void *argv[] = {&args, &tiles_m, &tiles_n};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_tile_kernel<C>), grid, dim3(64 * C::NW), argv, 0,
+                           stream);
+}
+
+// 256 x 256 (eight waves), 128 x 128, 64 x 128 and 32 x 128 (four waves).
+enum TileSize { kTile256, kTile128, kTile64, kTile32 };
+
+// Few rows a group: the tile that holds them, so that little of it is empty.
+// Otherwise the largest tile that still gives every compute unit one.
+inline TileSize tile_size(const GroupedParams &p, bool dma) {
+    const int64_t groups = p.ends != nullptr ? p.groups : 1, rows = p.M / (groups > 0 ? groups : 1);
+    auto tiles = [&](int bm, int bn) {
+        return most_row_tiles(p.M, p.groups, bm, p.ends != nullptr) * ((p.N + bn - 1) / bn);
+    };
+    if (rows <= 32) return kTile32;
+    if (rows <= 64 || tiles(128, 128) < 256) return kTile64;
+    return dma && tiles(256, 256) >= 256 ? kTile256 : kTile128;
+}
+
+template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParams &p, hipStream_t s) {
+    switch (tile_size(p, DMA)) {
+        case kTile256:
+            if constexpr (DMA) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
+        case kTile128: return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
+        case kTile64: return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
+        default: return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA>>(p, s);
+    }
+}
+template <int DT> hipError_t launch_typed(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t s) {
+    if (op_b == GEMM_OP_N) return dma ? launch_sized<DT, true, true>(p, s) : launch_sized<DT, true, false>(p, s);
+    return dma ? launch_sized<DT, false, true>(p, s) : launch_sized<DT, false, false>(p, s);
+}
+
+}  // namespace
+}  // namespace gemm
+
+#endif
