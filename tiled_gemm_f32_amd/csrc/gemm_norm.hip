@@ -45,16 +45,25 @@ template <> struct Io<GEMM_DTYPE_BF16F32> {
     }
 };
 
-// Up to 8 values from `src`, n of them valid (n <= 0: none; the rest read as
-// zero).  vec: every chunk of the operand starts on 16 bytes.
+// A chunk at any alignment of its elements: the hardware takes unaligned
+// 16-byte accesses, and rows of an odd length start anywhere.
+template <class V> struct __attribute__((packed, aligned(1))) Anywhere {
+    V v;
+};
+template <class V> __device__ __forceinline__ V get(const void *p) {
+    return reinterpret_cast<const Anywhere<V> *>(p)->v;
+}
+template <class V> __device__ __forceinline__ void put(void *p, V v) { reinterpret_cast<Anywhere<V> *>(p)->v = v; }
+
+// Up to 8 values, n of them valid (n <= 0: none; the rest read as zero).
 template <int DT>
-__device__ __forceinline__ typename Io<DT>::Raw load_raw(const void *base, int64_t at, int n, bool vec) {
+__device__ __forceinline__ typename Io<DT>::Raw load_raw(const void *base, int64_t at, int n) {
     typedef typename Io<DT>::T T;
     typedef typename Io<DT>::Raw Raw;
     const T *src = static_cast<const T *>(base) + at;
     Raw r = {};
-    if (vec && n >= kChunk) {
-        r = *reinterpret_cast<const Raw *>(src);
+    if (n >= kChunk) {
+        r = get<Raw>(src);
     } else if constexpr (DT == GEMM_DTYPE_F32) {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e)
@@ -67,21 +76,21 @@ __device__ __forceinline__ typename Io<DT>::Raw load_raw(const void *base, int64
     return r;
 }
 template <int DT>
-__device__ __forceinline__ f32x8 load8(const void *base, int64_t at, int n, bool vec) {
-    return Io<DT>::values(load_raw<DT>(base, at, n, vec));
+__device__ __forceinline__ f32x8 load8(const void *base, int64_t at, int n) {
+    return Io<DT>::values(load_raw<DT>(base, at, n));
 }
 template <int DT>
-__device__ __forceinline__ void store8(void *base, int64_t at, f32x8 v, int n, bool vec) {
+__device__ __forceinline__ void store8(void *base, int64_t at, f32x8 v, int n) {
     typedef typename Io<DT>::T T;
     T *dst = static_cast<T *>(base) + at;
-    if (vec && n >= kChunk) {
+    if (n >= kChunk) {
         if constexpr (DT == GEMM_DTYPE_F32) {
-            *reinterpret_cast<f32x8 *>(dst) = v;
+            put(dst, v);
         } else {
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = (uint32_t)to_bf16(v[2 * i]) | ((uint32_t)to_bf16(v[2 * i + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(dst) = w;
+            put(dst, w);
         }
     } else {
 #pragma unroll
@@ -135,9 +144,9 @@ __device__ __forceinline__ u32x2 codes8(f32x8 v, float inv) {
     }
     return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t *dst, u32x2 w, int n, bool vec) {
-    if (vec && n >= kChunk) {
-        *reinterpret_cast<u32x2 *>(dst) = w;
+__device__ __forceinline__ void store_codes(uint8_t *dst, u32x2 w, int n) {
+    if (n >= kChunk) {
+        put(dst, w);
     } else {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e)
@@ -147,10 +156,6 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, u32x2 w, int n, bool v
 
 // Workgroup number of a launch folded into two grid dimensions (fold below).
 __device__ __forceinline__ int64_t folded_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
-
-__host__ __device__ inline bool vectors(const void *p, int64_t ld, int bytes, int esz) {
-    return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && (ld * esz) % bytes == 0;
-}
 
 // Sum over a team of THREADS threads (one or more whole waves) of a workgroup
 // that is one team, or of one wave.  `red`: one float a wave, two sets used
@@ -170,34 +175,28 @@ template <int THREADS> __device__ __forceinline__ float team_sum(float v, float 
 
 // One chunk's y out: fp32, bf16, or codes with their block's scale.  A chunk
 // that is wholly past the row's end takes part in the lane rotations only.
-__device__ __forceinline__ void put_norm(const NormParams &p, int64_t row, int64_t col, f32x8 y, int n, bool vec_o) {
+__device__ __forceinline__ void put_norm(const NormParams &p, int64_t row, int64_t col, f32x8 y, int n) {
     if (p.out_type == GEMM_OUT_FP8) {
         const float amax = fmaxf(max16(finite_max(y)), kMinAmax);
         const u32x2 w = codes8(y, kE4m3Max / amax);
         if (n > 0) {
-            store_codes(static_cast<uint8_t *>(p.out) + row * p.ldo + col, w, n, vec_o);
+            store_codes(static_cast<uint8_t *>(p.out) + row * p.ldo + col, w, n);
             if ((col & (GEMM_SCALE_BLOCK - 1)) == 0)
                 p.scales[row * p.ld_scales + col / GEMM_SCALE_BLOCK] = amax / kE4m3Max;
         }
     } else if (p.out_type == GEMM_OUT_BF16) {
-        store8<GEMM_DTYPE_BF16F32>(p.out, row * p.ldo + col, y, n, vec_o);
+        store8<GEMM_DTYPE_BF16F32>(p.out, row * p.ldo + col, y, n);
     } else {
-        store8<GEMM_DTYPE_F32>(p.out, row * p.ldo + col, y, n, vec_o);
+        store8<GEMM_DTYPE_F32>(p.out, row * p.ldo + col, y, n);
     }
-}
-
-__device__ __forceinline__ bool norm_vec_out(const NormParams &p) {
-    return p.out_type == GEMM_OUT_FP8    ? vectors(p.out, p.ldo, 8, 1)
-           : p.out_type == GEMM_OUT_BF16 ? vectors(p.out, p.ldo, 16, 2)
-                                         : vectors(p.out, p.ldo, 16, 4);
 }
 
 // s of one chunk, rounded to the operands' type as it is stored.
 template <int DT>
-__device__ __forceinline__ f32x8 norm_sum(const NormParams &p, int64_t row, int64_t col, int n, bool vx, bool vr) {
-    f32x8 v = load8<DT>(p.x, row * p.ldx + col, n, vx);
+__device__ __forceinline__ f32x8 norm_sum(const NormParams &p, int64_t row, int64_t col, int n) {
+    f32x8 v = load8<DT>(p.x, row * p.ldx + col, n);
     if (p.residual != nullptr) {
-        const f32x8 r = load8<DT>(p.residual, row * p.ldr + col, n, vr);
+        const f32x8 r = load8<DT>(p.residual, row * p.ldr + col, n);
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) v[e] = Io<DT>::widen(Io<DT>::narrow(v[e] + r[e]));
     }
@@ -209,23 +208,20 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
 rms_norm_kernel(NormParams p) {
     constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;
     __shared__ float red[THREADS / 64];
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int64_t row = folded_block() * TEAMS + (TEAMS > 1 ? threadIdx.x / THREADS : 0);
     const int t = threadIdx.x % THREADS;
     if (row >= p.M) return;                    // the whole team together
-    const bool vx = vectors(p.x, p.ldx, 16, esz), vr = vectors(p.residual, p.ldr, 16, esz);
-    const bool vw = vectors(p.weight, 0, 16, esz), vs = vectors(p.sum, p.ld_sum, 16, esz), vo = norm_vec_out(p);
     const int N = (int)p.N;
     f32x8 s[PER], w[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        s[i] = norm_sum<DT>(p, row, col, N - col, vx, vr);
+        s[i] = norm_sum<DT>(p, row, col, N - col);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        w[i] = load8<DT>(p.weight, col, N - col, vw);
+        w[i] = load8<DT>(p.weight, col, N - col);
     }
     float sq = 0.0f;
 #pragma unroll
@@ -233,7 +229,7 @@ rms_norm_kernel(NormParams p) {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) sq = fmaf(s[i][e], s[i][e], sq);
         const int col = kChunk * (t + i * THREADS);
-        if (p.sum != nullptr) store8<DT>(p.sum, row * p.ld_sum + col, s[i], N - col, vs);
+        if (p.sum != nullptr) store8<DT>(p.sum, row * p.ld_sum + col, s[i], N - col);
     }
     const float r = 1.0f / sqrtf(team_sum<THREADS>(sq, red, 0) / (float)N + p.eps);
 #pragma unroll
@@ -242,7 +238,7 @@ rms_norm_kernel(NormParams p) {
         f32x8 y;
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) y[e] = s[i][e] * r * w[i][e];
-        put_norm(p, row, col, y, N - col, vo);
+        put_norm(p, row, col, y, N - col);
     }
 }
 
@@ -251,15 +247,12 @@ template <int DT>
 __global__ void __launch_bounds__(1024)
 rms_norm_long_kernel(NormParams p) {
     __shared__ float red[16];
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int64_t row = folded_block();
     if (row >= p.M) return;
-    const bool vx = vectors(p.x, p.ldx, 16, esz), vr = vectors(p.residual, p.ldr, 16, esz);
-    const bool vw = vectors(p.weight, 0, 16, esz), vs = vectors(p.sum, p.ld_sum, 16, esz), vo = norm_vec_out(p);
     float sq = 0.0f;
     for (int64_t col = kChunk * threadIdx.x; col < p.N; col += kChunk * 1024) {
         const int n = (int)min((int64_t)kChunk, p.N - col);
-        const f32x8 s = norm_sum<DT>(p, row, col, n, vx, vr);
+        const f32x8 s = norm_sum<DT>(p, row, col, n);
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) sq = fmaf(s[e], s[e], sq);
     }
@@ -270,13 +263,13 @@ rms_norm_long_kernel(NormParams p) {
         const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.N - col));
         f32x8 y = {};
         if (n > 0) {
-            const f32x8 s = norm_sum<DT>(p, row, col, n, vx, vr);
-            const f32x8 w = load8<DT>(p.weight, col, n, vw);
-            if (p.sum != nullptr) store8<DT>(p.sum, row * p.ld_sum + col, s, n, vs);
+            const f32x8 s = norm_sum<DT>(p, row, col, n);
+            const f32x8 w = load8<DT>(p.weight, col, n);
+            if (p.sum != nullptr) store8<DT>(p.sum, row * p.ld_sum + col, s, n);
 #pragma unroll
             for (int e = 0; e < kChunk; ++e) y[e] = s[e] * r * w[e];
         }
-        put_norm(p, row, col, y, n, vo);
+        put_norm(p, row, col, y, n);
     }
 }
 
@@ -289,12 +282,8 @@ rms_norm_backward_kernel(NormGradParams p) {
     constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;
     typedef typename Io<DT>::Raw Raw;
     __shared__ float red[4 * (THREADS / 64)];
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int team = blockIdx.x * TEAMS + (TEAMS > 1 ? threadIdx.x / THREADS : 0), teams = gridDim.x * TEAMS;
     const int t = threadIdx.x % THREADS;
-    const bool vy = vectors(p.dy, p.lddy, 16, esz), vs = vectors(p.s, p.lds, 16, esz);
-    const bool vw = vectors(p.weight, 0, 16, esz), vd = vectors(p.ds, p.ldds, 16, esz);
-    const bool vx = vectors(p.dx, p.lddx, 16, esz);
     const int N = (int)p.N;
     const float inv_n = 1.0f / (float)N;
     f32x8 w[PER], dw[PER];
@@ -303,15 +292,15 @@ rms_norm_backward_kernel(NormGradParams p) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int col = kChunk * (t + i * THREADS);
-            dy[i] = load_raw<DT>(p.dy, row * p.lddy + col, N - col, vy);
-            s[i] = load_raw<DT>(p.s, row * p.lds + col, N - col, vs);
-            if (p.ds != nullptr) ds[i] = load_raw<DT>(p.ds, row * p.ldds + col, N - col, vd);
+            dy[i] = load_raw<DT>(p.dy, row * p.lddy + col, N - col);
+            s[i] = load_raw<DT>(p.s, row * p.lds + col, N - col);
+            if (p.ds != nullptr) ds[i] = load_raw<DT>(p.ds, row * p.ldds + col, N - col);
         }
     };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        w[i] = load8<DT>(p.weight, col, N - col, vw);
+        w[i] = load8<DT>(p.weight, col, N - col);
         dw[i] = f32x8{};
         ds[i] = Raw{};
     }
@@ -358,14 +347,14 @@ rms_norm_backward_kernel(NormGradParams p) {
                 dx[e] = fmaf(r, fmaf(-along, sv[e] * r, yv[e] * w[i][e]), dv[e]);
                 dw[i][e] = fmaf(yv[e] * r, sv[e], dw[i][e]);
             }
-            store8<DT>(p.dx, row * p.lddx + col, dx, N - col, vx);
+            store8<DT>(p.dx, row * p.lddx + col, dx, N - col);
         }
     }
     if (p.dweight == nullptr) return;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        store8<GEMM_DTYPE_F32>(p.partials, (int64_t)team * N + col, dw[i], N - col, N % 4 == 0);
+        store8<GEMM_DTYPE_F32>(p.partials, (int64_t)team * N + col, dw[i], N - col);
     }
 }
 
@@ -376,19 +365,15 @@ template <int DT>
 __global__ void __launch_bounds__(1024)
 rms_norm_backward_long_kernel(NormGradParams p) {
     __shared__ float red[64];
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int team = blockIdx.x, teams = gridDim.x;
-    const bool vy = vectors(p.dy, p.lddy, 16, esz), vs = vectors(p.s, p.lds, 16, esz);
-    const bool vw = vectors(p.weight, 0, 16, esz), vd = vectors(p.ds, p.ldds, 16, esz);
-    const bool vx = vectors(p.dx, p.lddx, 16, esz);
     const float inv_n = 1.0f / (float)p.N;
     int set = 0;
     for (int64_t row = team; row < p.M; row += teams, set ^= 2) {
         float sq = 0.0f, gs = 0.0f;
         for (int64_t col = kChunk * threadIdx.x; col < p.N; col += kChunk * 1024) {
             const int n = (int)min((int64_t)kChunk, p.N - col);
-            const f32x8 sv = load8<DT>(p.s, row * p.lds + col, n, vs), yv = load8<DT>(p.dy, row * p.lddy + col, n, vy);
-            const f32x8 w = load8<DT>(p.weight, col, n, vw);
+            const f32x8 sv = load8<DT>(p.s, row * p.lds + col, n), yv = load8<DT>(p.dy, row * p.lddy + col, n);
+            const f32x8 w = load8<DT>(p.weight, col, n);
 #pragma unroll
             for (int e = 0; e < kChunk; ++e) {
                 sq = fmaf(sv[e], sv[e], sq);
@@ -412,41 +397,44 @@ rms_norm_backward_long_kernel(NormGradParams p) {
         const float along = r * (gs * inv_n);      // of the size of g: r^3 on its own could overflow
         for (int64_t col = kChunk * threadIdx.x; col < p.N; col += kChunk * 1024) {
             const int n = (int)min((int64_t)kChunk, p.N - col);
-            const f32x8 sv = load8<DT>(p.s, row * p.lds + col, n, vs), yv = load8<DT>(p.dy, row * p.lddy + col, n, vy);
-            const f32x8 w = load8<DT>(p.weight, col, n, vw);
+            const f32x8 sv = load8<DT>(p.s, row * p.lds + col, n), yv = load8<DT>(p.dy, row * p.lddy + col, n);
+            const f32x8 w = load8<DT>(p.weight, col, n);
             f32x8 dv = {}, dx;
-            if (p.ds != nullptr) dv = load8<DT>(p.ds, row * p.ldds + col, n, vd);
+            if (p.ds != nullptr) dv = load8<DT>(p.ds, row * p.ldds + col, n);
             if (p.dweight != nullptr) {
-                const bool vp = p.N % 4 == 0;
                 f32x8 dw = {};
-                if (row != team) dw = load8<GEMM_DTYPE_F32>(p.partials, team * p.N + col, n, vp);
+                if (row != team) dw = load8<GEMM_DTYPE_F32>(p.partials, team * p.N + col, n);
 #pragma unroll
                 for (int e = 0; e < kChunk; ++e) dw[e] = fmaf(yv[e] * r, sv[e], dw[e]);
-                store8<GEMM_DTYPE_F32>(p.partials, team * p.N + col, dw, n, vp);
+                store8<GEMM_DTYPE_F32>(p.partials, team * p.N + col, dw, n);
             }
 #pragma unroll
             for (int e = 0; e < kChunk; ++e) dx[e] = fmaf(r, fmaf(-along, sv[e] * r, yv[e] * w[e]), dv[e]);
-            store8<DT>(p.dx, row * p.lddx + col, dx, n, vx);
+            store8<DT>(p.dx, row * p.lddx + col, dx, n);
         }
     }
 }
 
-// dweight[j] = sum of `parts` partial rows, in order: 32 columns a workgroup,
-// 8 threads a column each adding every eighth row, then their sums in turn.
-__global__ void __launch_bounds__(256)
+// dweight[j] = sum of `parts` partial rows in a fixed order: 32 columns a
+// workgroup, 32 threads a column each adding every 32nd row, eight rows in
+// flight, then the threads' sums in turn.
+__global__ void __launch_bounds__(1024)
 dweight_kernel(const float *partials, float *dweight, int parts, int64_t N) {
-    __shared__ float part[8][32];
+    __shared__ float part[32][32];
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t col = (int64_t)blockIdx.x * 32 + c;
-    float s = 0.0f;
+    float s[8] = {};
     if (col < N)
-        for (int i = g; i < parts; i += 8) s += partials[(int64_t)i * N + col];
-    part[g][c] = s;
+        for (int i = g; i < parts; i += 256) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s[u] += i + 32 * u < parts ? partials[(int64_t)(i + 32 * u) * N + col] : 0.0f;
+        }
+    part[g][c] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     if (g == 0 && col < N) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += part[i][c];
+        for (int i = 0; i < 32; ++i) t += part[i][c];
         dweight[col] = t;
     }
 }
@@ -455,17 +443,17 @@ dweight_kernel(const float *partials, float *dweight, int parts, int64_t N) {
 template <int DT>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(QuantParams p, int64_t blocks, int per_row) {
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int64_t b = folded_block() * 16 + threadIdx.x / 16;
     if (b >= blocks) return;                   // sixteen lanes together
-    const int64_t row = b / per_row;
+    // 32-bit division where it will do: the 64-bit one is some hundred instructions.
+    const int64_t row = blocks >> 32 == 0 ? (int64_t)((uint32_t)b / (uint32_t)per_row) : b / per_row;
     const int j = (int)(b - row * per_row);
     const int64_t col = (int64_t)j * GEMM_SCALE_BLOCK + kChunk * (threadIdx.x & 15);
     const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.K - col));
-    const f32x8 v = load8<DT>(p.x, row * p.ldx + col, n, vectors(p.x, p.ldx, 16, esz));
+    const f32x8 v = load8<DT>(p.x, row * p.ldx + col, n);
     const float amax = fmaxf(max16(finite_max(v)), kMinAmax);
     const u32x2 w = codes8(v, kE4m3Max / amax);
-    if (n > 0) store_codes(p.q + row * p.ldq + col, w, n, vectors(p.q, p.ldq, 8, 1));
+    if (n > 0) store_codes(p.q + row * p.ldq + col, w, n);
     if ((threadIdx.x & 15) == 0) p.scales[row * p.lds + j] = amax / kE4m3Max;
 }
 
@@ -474,7 +462,6 @@ template <int DT>
 __global__ void __launch_bounds__(256)
 quantize_tiles_kernel(QuantParams p, int64_t tiles, int per_row) {
     __shared__ float red[4];
-    constexpr int esz = (int)sizeof(typename Io<DT>::T);
     const int64_t b = folded_block();
     if (b >= tiles) return;                    // the whole workgroup
     const int64_t tile_row = b / per_row;
@@ -482,13 +469,12 @@ quantize_tiles_kernel(QuantParams p, int64_t tiles, int per_row) {
     const int64_t row0 = tile_row * GEMM_SCALE_BLOCK + threadIdx.x / 16;
     const int64_t col = (int64_t)tile_col * GEMM_SCALE_BLOCK + kChunk * (threadIdx.x & 15);
     const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.K - col));
-    const bool vx = vectors(p.x, p.ldx, 16, esz), vq = vectors(p.q, p.ldq, 8, 1);
     f32x8 v[8];
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t row = row0 + 16 * i;
-        v[i] = load8<DT>(p.x, row * p.ldx + col, row < p.M ? n : 0, vx);
+        v[i] = load8<DT>(p.x, row * p.ldx + col, row < p.M ? n : 0);
         amax = fmaxf(amax, finite_max(v[i]));
     }
     amax = max16(amax);
@@ -500,7 +486,7 @@ quantize_tiles_kernel(QuantParams p, int64_t tiles, int per_row) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t row = row0 + 16 * i;
-        if (row < p.M && n > 0) store_codes(p.q + row * p.ldq + col, codes8(v[i], kE4m3Max / amax), n, vq);
+        if (row < p.M && n > 0) store_codes(p.q + row * p.ldq + col, codes8(v[i], kE4m3Max / amax), n);
     }
     if (threadIdx.x == 0) p.scales[tile_row * p.lds + tile_col] = amax / kE4m3Max;
 }
@@ -576,7 +562,7 @@ hipError_t launch_rms_norm_backward(const NormGradParams &p, hipStream_t s) {
     if (p.M > 0)
         err = p.dtype == GEMM_DTYPE_F32 ? grad_type<GEMM_DTYPE_F32>(p, s) : grad_type<GEMM_DTYPE_BF16F32>(p, s);
     if (err != hipSuccess || p.dweight == nullptr) return err;
-    return go(&dweight_kernel, dim3((unsigned)((p.N + 31) / 32)), 256, s, (const float *)p.partials, p.dweight,
+    return go(&dweight_kernel, dim3((unsigned)((p.N + 31) / 32)), 1024, s, (const float *)p.partials, p.dweight,
               norm_grad_partials(p.M, p.N), p.N);
 }
 

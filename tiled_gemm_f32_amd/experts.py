@@ -20,41 +20,58 @@ from ._lib import (
     gemm_quantize, gemm_rms_norm, gemm_rms_norm_backward, gemm_rms_norm_workspace_size)
 
 
+# A call costs the host about as long as a small kernel runs, so the checks
+# below are written for the common case: one attribute of a tensor read once,
+# devices compared as numbers, messages made only when something is wrong.
+
 def _float_type(t, what: str) -> int:
     import torch
-    if t.dtype == torch.float32:
-        return GEMM_DTYPE_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return GEMM_DTYPE_BF16F32
+    if t.dtype is torch.float32:
+        return GEMM_DTYPE_F32
     raise TypeError(f"{what} must be float32 or bfloat16 (got {t.dtype})")
 
 
 def _out_type(dtype, what: str) -> int:
     import torch
-    kinds = {torch.float32: GEMM_OUT_F32, torch.bfloat16: GEMM_OUT_BF16, torch.float8_e4m3fn: GEMM_OUT_FP8}
-    if dtype not in kinds:
-        raise TypeError(f"{what} must be float32, bfloat16 or float8_e4m3fn (got {dtype})")
-    return kinds[dtype]
+    if dtype is torch.bfloat16:
+        return GEMM_OUT_BF16
+    if dtype is torch.float8_e4m3fn:
+        return GEMM_OUT_FP8
+    if dtype is torch.float32:
+        return GEMM_OUT_F32
+    raise TypeError(f"{what} must be float32, bfloat16 or float8_e4m3fn (got {dtype})")
 
 
 def _ld(t, what: str) -> int:
     """Leading dimension of a matrix (or of each matrix of a 3-D tensor)."""
+    strides = t.stride()
     rows, cols = t.shape[-2:]
+    if rows > 1 and cols > 1 and strides[-1] == 1 and strides[-2] >= cols:
+        return strides[-2]
     if t.numel() == 0:
         return max(cols, 1)
-    if cols > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what} must have unit stride along its rows; got strides {t.stride()}")
-    if rows > 1 and t.stride(-2) < max(cols, 1):
-        raise ValueError(f"{what} must be row-major with rows that do not overlap; got strides {t.stride()}")
-    return t.stride(-2) if rows > 1 else max(cols, 1)
+    if cols > 1 and strides[-1] != 1:
+        raise ValueError(f"{what} must have unit stride along its rows; got strides {strides}")
+    if rows > 1 and strides[-2] < max(cols, 1):
+        raise ValueError(f"{what} must be row-major with rows that do not overlap; got strides {strides}")
+    return strides[-2] if rows > 1 else max(cols, 1)
 
 
-def _check(t, what: str, device, shape=None, dtype=None, dim: int = 2):
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{what} must be a tensor on {device if device.type == 'cuda' else 'the GPU'}")
-    if dtype is not None and t.dtype != dtype:
+def _device(t, what: str) -> int:
+    """Number of the GPU a tensor is on."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a tensor on the GPU")
+    return t.get_device()
+
+
+def _check(t, what: str, device: int, shape=None, dtype=None, dim: int = 2):
+    if t.get_device() != device or not t.is_cuda:
+        raise ValueError(f"{what} must be a tensor on cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if shape is None and t.dim() != dim:
         raise ValueError(f"{what} must be {dim}-D, got shape {tuple(t.shape)}")
@@ -67,21 +84,26 @@ def _blocks(n: int) -> int:
 def _codes(rows: int, cols: int, device):
     """rows x cols codes whose rows start on 16 bytes, which the matrix-core paths ask for."""
     import torch
+    if cols % 16 == 0:
+        return torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
     return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
 
 
-def _call(name: str, device, stream, made, fn, *args):
-    """fn(*args, stream) on `device`; tensors in `made` were allocated for this call."""
+def _call(name: str, device: int, stream, made, fn, *args):
+    """fn(*args, stream) on GPU `device`; tensors in `made` were allocated for this call."""
     import torch
-    with torch.cuda.device(device):
-        current = torch.cuda.current_stream(device).cuda_stream
-        if stream is None:
-            stream = current
-        elif stream != current:
-            other = torch.cuda.ExternalStream(stream, device=device)
-            for t in made:
-                t.record_stream(other)
+    current = torch._C._cuda_getCurrentRawStream(device)
+    if stream is None:
+        stream = current
+    elif stream != current:
+        other = torch.cuda.ExternalStream(stream, device=device)
+        for t in made:
+            t.record_stream(other)
+    if torch._C._cuda_getDevice() == device:
         st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
     if st != GEMM_OK:
         raise GemmError(st, name)
 
@@ -95,7 +117,8 @@ def quantize(x, block_rows: int = 1, out=None, scales=None, stream=None):
     allocated here have rows padded to 16 bytes."""
     import torch
     dt = _float_type(x, "x")
-    _check(x, "x", x.device)
+    device = _device(x, "x")
+    _check(x, "x", device)
     if block_rows not in (1, GEMM_SCALE_BLOCK):
         raise ValueError(f"block_rows is 1 or {GEMM_SCALE_BLOCK} (got {block_rows})")
     M, K = x.shape
@@ -106,9 +129,9 @@ def quantize(x, block_rows: int = 1, out=None, scales=None, stream=None):
     if scales is None:
         scales = torch.empty((-(-M // block_rows), _blocks(K)), dtype=torch.float32, device=x.device)
         made.append(scales)
-    _check(out, "out", x.device, (M, K), torch.float8_e4m3fn)
-    _check(scales, "scales", x.device, (-(-M // block_rows), _blocks(K)), torch.float32)
-    _call("quantize", x.device, stream, made, gemm_quantize, dt, block_rows, M, K, x.data_ptr(), _ld(x, "x"),
+    _check(out, "out", device, (M, K), torch.float8_e4m3fn)
+    _check(scales, "scales", device, (-(-M // block_rows), _blocks(K)), torch.float32)
+    _call("quantize", device, stream, made, gemm_quantize, dt, block_rows, M, K, x.data_ptr(), _ld(x, "x"),
           out.data_ptr(), _ld(out, "out"), scales.data_ptr(), _ld(scales, "scales"))
     return out, scales
 
@@ -125,19 +148,20 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
     a scale for every 128 columns of a row, otherwise it is None."""
     import torch
     dt = _float_type(x, "x")
-    _check(x, "x", x.device)
+    device = _device(x, "x")
+    _check(x, "x", device)
     M, N = x.shape
-    _check(weight, "weight", x.device, (N,), x.dtype)
+    _check(weight, "weight", device, (N,), x.dtype)
     if N > 1 and weight.stride(0) != 1:
         raise ValueError("weight must be contiguous")
     made = []
     if residual is not None:
-        _check(residual, "residual", x.device, (M, N), x.dtype)
+        _check(residual, "residual", device, (M, N), x.dtype)
         if summed is None:
             summed = torch.empty((M, N), dtype=x.dtype, device=x.device)
             made.append(summed)
     if summed is not None:
-        _check(summed, "summed", x.device, (M, N), x.dtype)
+        _check(summed, "summed", device, (M, N), x.dtype)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     kind = _out_type(out.dtype if out is not None else out_dtype or x.dtype, "out")
@@ -145,15 +169,15 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
         out = _codes(M, N, x.device) if kind == GEMM_OUT_FP8 else torch.empty((M, N), dtype=out_dtype or x.dtype,
                                                                               device=x.device)
         made.append(out)
-    _check(out, "out", x.device, (M, N))
+    _check(out, "out", device, (M, N))
     if kind == GEMM_OUT_FP8:
         if scales is None:
             scales = torch.empty((M, _blocks(N)), dtype=torch.float32, device=x.device)
             made.append(scales)
-        _check(scales, "scales", x.device, (M, _blocks(N)), torch.float32)
+        _check(scales, "scales", device, (M, _blocks(N)), torch.float32)
     elif scales is not None:
         raise ValueError("scales go with a float8_e4m3fn output")
-    _call("rms_norm", x.device, stream, made, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"),
+    _call("rms_norm", device, stream, made, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"),
           residual.data_ptr() if residual is not None else 0, _ld(residual, "residual") if residual is not None else 0,
           weight.data_ptr(), float(eps), summed.data_ptr() if summed is not None else 0,
           _ld(summed, "summed") if summed is not None else 0, kind, out.data_ptr(), _ld(out, "out"),
@@ -171,19 +195,20 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
     is not wanted."""
     import torch
     dt = _float_type(dy, "dy")
-    _check(dy, "dy", dy.device)
+    device = _device(dy, "dy")
+    _check(dy, "dy", device)
     M, N = dy.shape
-    _check(summed, "summed", dy.device, (M, N), dy.dtype)
-    _check(weight, "weight", dy.device, (N,), dy.dtype)
+    _check(summed, "summed", device, (M, N), dy.dtype)
+    _check(weight, "weight", device, (N,), dy.dtype)
     if N > 1 and weight.stride(0) != 1:
         raise ValueError("weight must be contiguous")
     if dsum is not None:
-        _check(dsum, "dsum", dy.device, (M, N), dy.dtype)
+        _check(dsum, "dsum", device, (M, N), dy.dtype)
     made = []
     if dx is None:
         dx = torch.empty((M, N), dtype=dy.dtype, device=dy.device)
         made.append(dx)
-    _check(dx, "dx", dy.device, (M, N), dy.dtype)
+    _check(dx, "dx", device, (M, N), dy.dtype)
     dweight = ws = None
     need = 0
     if want_dweight:
@@ -191,7 +216,7 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
         dweight = torch.empty(N, dtype=torch.float32, device=dy.device)
         ws = torch.empty(max(need, 4), dtype=torch.uint8, device=dy.device)
         made += [dweight, ws]
-    _call("rms_norm_backward", dy.device, stream, made, gemm_rms_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
+    _call("rms_norm_backward", device, stream, made, gemm_rms_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
           summed.data_ptr(), _ld(summed, "summed"), weight.data_ptr(), float(eps),
           dsum.data_ptr() if dsum is not None else 0, _ld(dsum, "dsum") if dsum is not None else 0, dx.data_ptr(),
           _ld(dx, "dx"), dweight.data_ptr() if dweight is not None else 0, ws.data_ptr() if ws is not None else 0, need)
@@ -200,19 +225,20 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
 
 def _strides(scales, lead: int, shape, what: str):
     """Strides of a scale tensor's last two dimensions, after checking its shape."""
-    if tuple(scales.shape) != tuple(shape):
+    if scales.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(scales.shape)}")
-    return scales.stride(lead), scales.stride(lead + 1)
+    strides = scales.stride()
+    return strides[lead], strides[lead + 1]
 
 
-def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int):
+def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int, device: int):
     """The gemm_block_scales of a call.  b_scales follows B as it is stored:
     [group,] blocks of B's rows, blocks of its columns."""
     import torch
     for t, what in ((a_scales, "a_scales"), (b_scales, "b_scales")):
         if t is None:
             raise ValueError(f"float8_e4m3fn operands need {what}")
-        _check(t, what, A.device, t.shape, torch.float32)
+        _check(t, what, device, t.shape, torch.float32)
     a_row, a_block = _strides(a_scales, 0, (M, _blocks(K)), "a_scales")
     lead = B.dim() - 2
     shape = tuple(B.shape[:lead]) + (_blocks(B.shape[-2]), _blocks(B.shape[-1]))
@@ -222,7 +248,7 @@ def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int):
                        b_scales.stride(0) if lead else 0)
 
 
-def _product_out(M: int, N: int, out, out_dtype, default, device, made):
+def _product_out(M: int, N: int, out, out_dtype, default, like, device: int, made):
     import torch
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -230,7 +256,7 @@ def _product_out(M: int, N: int, out, out_dtype, default, device, made):
     if kind == GEMM_OUT_FP8:
         raise TypeError("out must be float32 or bfloat16")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or default, device=device)
+        out = torch.empty((M, N), dtype=out_dtype or default, device=like.device)
         made.append(out)
     _check(out, "out", device, (M, N))
     return out, kind
@@ -247,21 +273,22 @@ def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, ou
     import torch
     if op_b not in ("N", "T"):
         raise ValueError("op_b is 'N' or 'T'")
-    _check(A, "A", A.device, dtype=torch.float8_e4m3fn)
-    _check(B, "B", A.device, dtype=torch.float8_e4m3fn)
+    device = _device(A, "A")
+    _check(A, "A", device, dtype=torch.float8_e4m3fn)
+    _check(B, "B", device, dtype=torch.float8_e4m3fn)
     M, K = A.shape
     N, K2 = B.shape if op_b == "T" else (B.shape[1], B.shape[0])
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, op_b={op_b} {tuple(B.shape)}")
-    sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K)
+    sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K, device)
     made = []
-    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A.device, made)
-    _call("block_gemm", A.device, stream, made, gemm_block_scaled, GEMM_OP_T if op_b == "T" else GEMM_OP_N, M, N, K,
+    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device, made)
+    _call("block_gemm", device, stream, made, gemm_block_scaled, GEMM_OP_T if op_b == "T" else GEMM_OP_N, M, N, K,
           float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), sc, kind, out.data_ptr(), _ld(out, "out"))
     return out
 
 
-def _check_ends(ends, device, groups: int):
+def _check_ends(ends, device: int, groups: int):
     import torch
     _check(ends, "ends", device, (groups,), torch.int32)
     if groups > 1 and ends.stride(0) != 1:
@@ -283,22 +310,23 @@ def grouped_gemm(A, B, ends, a_scales=None, b_scales=None, op_b: str = "T", alph
         raise ValueError("op_b is 'N' or 'T'")
     fp8 = A.dtype == torch.float8_e4m3fn
     dt = GEMM_DTYPE_FP8F32 if fp8 else _float_type(A, "A")
-    _check(A, "A", A.device)
-    _check(B, "B", A.device, dtype=A.dtype, dim=3)
+    device = _device(A, "A")
+    _check(A, "A", device)
+    _check(B, "B", device, dtype=A.dtype, dim=3)
     M, K = A.shape
     groups = B.shape[0]
     N, K2 = B.shape[1:] if op_b == "T" else (B.shape[2], B.shape[1])
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, op_b={op_b} {tuple(B.shape)}")
-    _check_ends(ends, A.device, groups)
+    _check_ends(ends, device, groups)
     sc = None
     if fp8:
-        sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K)
+        sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K, device)
     elif a_scales is not None or b_scales is not None:
         raise ValueError("scales go with float8_e4m3fn operands")
     made = []
-    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A.device, made)
-    _call("grouped_gemm", A.device, stream, made, gemm_grouped, dt, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
+    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A, device, made)
+    _call("grouped_gemm", device, stream, made, gemm_grouped, dt, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
           ends.data_ptr(), M, N, K, float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
           B.stride(0) if groups > 1 else 0, sc, kind, out.data_ptr(), _ld(out, "out"))
     return out
@@ -312,8 +340,9 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
     None; then beta must be 0).  A group without rows gives beta * out[g]."""
     import torch
     dt = _float_type(dy, "dy")
-    _check(dy, "dy", dy.device)
-    _check(x, "x", dy.device, dtype=dy.dtype)
+    device = _device(dy, "dy")
+    _check(dy, "dy", device)
+    _check(x, "x", device, dtype=dy.dtype)
     if x.shape[0] != dy.shape[0]:
         raise ValueError(f"dy and x differ in rows: {tuple(dy.shape)}, {tuple(x.shape)}")
     M, N = dy.shape
@@ -321,15 +350,15 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
     if ends.dim() != 1:
         raise ValueError(f"ends must be 1-D, got shape {tuple(ends.shape)}")
     groups = ends.shape[0]
-    _check_ends(ends, dy.device, groups)
+    _check_ends(ends, device, groups)
     made = []
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs an input out")
         out = torch.empty((groups, N, K), dtype=torch.float32, device=dy.device)
         made.append(out)
-    _check(out, "out", dy.device, (groups, N, K), torch.float32)
-    _call("grouped_wgrad", dy.device, stream, made, gemm_grouped_wgrad, dt, groups, ends.data_ptr(), M, N, K,
+    _check(out, "out", device, (groups, N, K), torch.float32)
+    _call("grouped_wgrad", device, stream, made, gemm_grouped_wgrad, dt, groups, ends.data_ptr(), M, N, K,
           float(alpha), dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), float(beta), out.data_ptr(),
           _ld(out, "out"), out.stride(0) if groups > 1 else 0)
     return out
