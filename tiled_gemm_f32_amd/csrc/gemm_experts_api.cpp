@@ -96,7 +96,7 @@ gemm_status run(const Product &c, gemm_stream_t stream) {
     // A row's bytes must hold one 16-byte load, whatever their alignment.
     const int64_t sz = (int64_t)esz;
     const bool tiles = c.dtype != GEMM_DTYPE_F32 && c.K * sz >= 16 && b_len * sz >= 16 && c.lda * sz < kMaxTileRow &&
-                       c.ldb * sz < kMaxTileRow && (c.sc == nullptr || c.sc->a_row * 4 < kMaxTileRow);
+                       c.ldb * sz < kMaxTileRow && (c.sc == nullptr || (c.sc->a_row < kMaxTileRow / 4 && c.sc->b_n < kMaxTileRow));
     const auto s = static_cast<hipStream_t>(stream);
     if (!tiles) return launched(gemm::launch_grouped_general(c.dtype, c.op_b, p, s));
     if (c.M == 1) p.lda = ceil_div(c.K * sz, 16) * 16 / sz;          // the stride of a single row is not used

@@ -30,9 +30,9 @@
 //     k row r at c ^ (r & 7), read with ds_read_b64_tr_b8.
 //
 // DMA: operands whose rows start on 16 bytes come by direct-to-LDS buffer
-// loads.  Rows and k past the ends fall outside the buffer resource (or get
-// an offset that does) and read as zero; a 16-byte chunk that straddles the
-// end of K is cut in LDS before it is read.  Otherwise (REG) chunks go
+// loads.  Rows past the ends fall outside the buffer resource and read as
+// zero; where K ends inside a slab, what the loads brought past it is zeroed
+// in LDS before it is read.  Otherwise (REG) chunks go
 // through registers with unaligned 16-byte loads, the last one of a row
 // loaded so that it ends with the row and shifted into place.
 #pragma once
@@ -77,7 +77,7 @@ struct Loader {
     int64_t ld;          // bytes
     int rows, len;       // elements
     uint32_t off;        // this lane's offset in load 0
-    int chunk;           // byte of the row (k or columns) this lane's chunk starts at
+    int chunk;           // REG: byte of the row (k or columns) this lane's chunk starts at
     u32x4 reg[C::DMA ? 1 : kLoads];
 
     __device__ __forceinline__ void init(int wave, int lane) {
@@ -92,24 +92,23 @@ struct Loader {
     }
     static __device__ __forceinline__ constexpr int byte_of(int j) { return KN ? kSlab * ((j * C::NW) / kGroups) : 0; }
 
-    // Slab t into `stage` (DMA) or into the staging registers.
-    __device__ __forceinline__ void fetch(int t, char *stage, int wave, int lane) {
-        if constexpr (C::DMA) {
-            // Bounds in 32 bits and without branches, which would cut the loop's schedule: a
-            // panel of 256 rows is below 2^31 bytes (checked on the host).
-            const int step = (int)ld;
-            const int left = KN ? len - t * C::BK : len * esz - t * kSlab;          // KN: rows, else bytes
-            const char *src = base + (KN ? (int64_t)t * C::BK * ld : (int64_t)t * kSlab);
-            const int wide = ((KN ? rows * esz : max(left, 0)) + 15) & ~15;         // whole chunks
-            const int deep = KN ? min(left, C::BK) : rows;
-            const rsrc_t rs = make_rsrc(src, (uint32_t)max(deep * step - (step - wide), 0));
-            uint32_t at = off;
-            if (!KN) at += (uint32_t)(chunk >= left) << 31;
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
-                                                         at + (uint32_t)(row_of(j) * step + byte_of(j)), 0, 0, 0);
-        } else {
+    // DMA: the buffer resource of slab t.  Bounds in 32 bits and without branches, which would
+    // cut the loop's schedule: a panel of 256 rows is below 2^31 bytes (checked on the host).
+    __device__ __forceinline__ rsrc_t source(int t) const {
+        const int step = (int)ld;
+        const int left = KN ? len - t * C::BK : len * esz - t * kSlab;          // KN: rows, else bytes
+        const char *src = base + (KN ? (int64_t)t * C::BK * ld : (int64_t)t * kSlab);
+        const int wide = ((KN ? rows * esz : max(left, 0)) + 15) & ~15;         // whole chunks
+        const int deep = KN ? min(left, C::BK) : rows;
+        return make_rsrc(src, (uint32_t)(max(deep * step - (step - wide), 0) & ~((left - 1) >> 31)));
+    }
+    __device__ __forceinline__ void load(const rsrc_t &r, char *stage, int wave, int j) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
+                                                 off + (uint32_t)(row_of(j) * (int)ld + byte_of(j)), 0, 0, 0);
+    }
+    // REG: slab t into the staging registers.
+    __device__ __forceinline__ void hold(int t, int wave, int lane) {
+        if constexpr (!C::DMA) {
             const int64_t k0 = (int64_t)t * C::BK;
             const int r0 = 8 * wave + (lane >> 3);
 #pragma unroll
@@ -138,17 +137,21 @@ struct Loader {
                 *reinterpret_cast<u32x4 *>(stage + (j * C::NW + wave) * 1024 + lane * 16) = reg[j];
         }
     }
-    // Zero the bytes past K of the chunk that straddles it, in every row of the slab that ends K.
-    __device__ __forceinline__ void cut(char *stage, int tail_bytes) const {
+    // Zero the bytes from `from` on in every row of a slab: those past K, where the loads
+    // have brought what follows a row in memory.
+    __device__ __forceinline__ void cut(char *stage, int from) const {
         if constexpr (!KN) {
-            for (int r = threadIdx.x; r < ROWS; r += 64 * C::NW) {
-                uint32_t *at = reinterpret_cast<uint32_t *>(stage + r * kSlab + 16 * ((tail_bytes >> 4) ^ ((r >> 1) & 7)));
+            for (int i = threadIdx.x; i < ROWS * 8; i += 64 * C::NW) {
+                const int r = i >> 3, c = i & 7;
+                u32x4 *at = reinterpret_cast<u32x4 *>(stage + r * kSlab + 16 * (c ^ ((r >> 1) & 7)));
+                if (16 * c + 16 <= from) continue;
+                u32x4 v = *at;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const int n = (tail_bytes & 15) - 4 * d;         // valid bytes from here on
-                    const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
-                    at[d] &= keep;
+                    const int n = from - 16 * c - 4 * d;            // valid bytes from here on
+                    v[d] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
                 }
+                *at = v;
             }
         }
     }
@@ -223,14 +226,12 @@ __device__ __forceinline__ FragOf<C::esz> read_frag(const char *panel, uint32_t 
 
 // B^T as the first operand and A^T as the second: register 4g + t of lane
 // (h, l32) is row l32, column 8g + 4h + t of the fragment.
-__device__ __forceinline__ f32x16 product_fp8(const FragOf<1> &a, const FragOf<1> &b) {
-    f32x16 part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.h[0], a.h[0], f32x16{}, 0, 0, 0, 0,
-                                                                   0, 0);
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.h[1], a.h[1], part, 0, 0, 0, 0, 0, 0);
+__device__ __forceinline__ f32x16 product_fp8(const FragOf<1> &a, const FragOf<1> &b, int half, f32x16 part) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.h[half], a.h[half], part, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 product_bf16(const FragOf<2> &a, const FragOf<2> &b, f32x16 acc) {
+__device__ __forceinline__ f32x16 product_bf16(const FragOf<2> &a, const FragOf<2> &b, int half, f32x16 acc) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 2 * half; i < 2 * half + 2; ++i)
         acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b.q[i]),
                                                       __builtin_bit_cast(bf16x8, a.q[i]), acc, 0, 0, 0);
     return acc;
@@ -289,33 +290,46 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     a.init(wave, lane);
     b.init(wave, lane);
 
-    // Slabs that are read as they land; with a chunk across K one more, cut first.
+    // Slabs that are read as they land; where K ends inside a slab, that one is cut first.
     const int len = a.len;
-    const bool cut = C::DMA && (!C::AKN || !C::BKN) && (int64_t)len * C::esz % 16 != 0;
+    const bool cut = C::DMA && (!C::AKN || !C::BKN) && len % C::BK != 0;
     const int nk = cut ? len / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
 
     const int l32 = lane & 31;
-    // Scales of the block that slab t is: a's of this lane's rows, b's of the wave's columns.
-    const float *sa = nullptr, *sb = nullptr;
-    uint32_t sa_off[FM];
-    float sc_a[2][FM], sc_b[2];
-    if (FP8) {
-        const int col0 = n0 + wn * 32 * FN;
-        sa = p.sc.a + (int64_t)row0 * p.sc.a_row;
-        sb = p.sc.b + (int64_t)group * p.sc.b_group + (int64_t)(col0 < p.N ? col0 / GEMM_SCALE_BLOCK : 0) * p.sc.b_n;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            sa_off[i] = (uint32_t)min((wm * FM + i) * 32 + l32, out_rows - 1) * (uint32_t)p.sc.a_row * 4u;
+    // Scales of the block that slab t is go to LDS as the slab does (of even
+    // slabs to one set, of odd ones to the other): wave w < kScaleA loads those
+    // of 64 rows, the next wave those of the tile's column blocks, the others
+    // nothing; five loads a wave and slab from global memory instead cost a
+    // tenth of the whole call.
+    constexpr int kScaleA = (BM + 63) / 64;
+    static_assert(!FP8 || kScaleA < NW, "a wave for each 64 rows and one for the columns");
+    // One array a set, as for the stages: the compiler can then tell that a read of one does
+    // not depend on loads still landing in the other.
+    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1];
+    const float *sc_base = nullptr;
+    int64_t sc_step = 0;
+    uint32_t sc_bytes = 0, sc_off = 0;
+    if constexpr (FP8) {
+        const bool of_a = wave < kScaleA, of_b = wave == kScaleA;
+        const int col_blocks = (out_cols + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK;
+        const int64_t each = of_a ? p.sc.a_row : p.sc.b_n;
+        const int count = of_a ? out_rows : col_blocks;
+        sc_base = of_a ? p.sc.a + (int64_t)row0 * p.sc.a_row
+                       : p.sc.b + (int64_t)group * p.sc.b_group + (int64_t)(n0 / GEMM_SCALE_BLOCK) * p.sc.b_n;
+        sc_step = of_a ? p.sc.a_block : p.sc.b_k;
+        sc_bytes = of_a || of_b ? (uint32_t)((count - 1) * (int)each + 1) * 4u : 0u;
+        sc_off = (uint32_t)min(of_a ? 64 * wave + lane : lane, count - 1) * (uint32_t)each * 4u;
     }
     const int blocks = (int)(((int64_t)len + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK);
-    auto scales = [&](int t, int set) __attribute__((always_inline)) {
+    auto load_scales = [&](int t, float *set) __attribute__((always_inline)) {
         if constexpr (FP8) {
-            const int k = min(t, blocks - 1);
-            sc_b[set] = sb[k * p.sc.b_k];
-            const rsrc_t col = make_rsrc(sa + k * p.sc.a_block, (uint32_t)((out_rows - 1) * (int)p.sc.a_row + 1) * 4u);
-#pragma unroll
-            for (int i = 0; i < FM; ++i) sc_a[set][i] = __builtin_bit_cast(float, load_b32(col, sa_off[i]));
+            const rsrc_t r = make_rsrc(sc_base + min(t, blocks - 1) * sc_step, sc_bytes);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(set + 64 * wave), 4, sc_off, 0, 0, 0);
         }
+    };
+    // a(row) * b(column block) for this lane's rows of fragment i, from a slab's set.
+    auto scale_of = [&](const float *set, int i) __attribute__((always_inline)) {
+        return FP8 ? set[(wm * FM + i) * 32 + l32] * set[64 * kScaleA + wn * 32 * FN / GEMM_SCALE_BLOCK] : 0.0f;
     };
 
     f32x16 acc[FM][FN];
@@ -328,26 +342,72 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     uint32_t a_base = frag_base<C, C::AKN>(wm * FM, lane), b_base = frag_base<C, C::BKN>(wn * FN, lane);
     auto read_a = [&](const char *st, int i) { return read_frag<C, C::AKN>(st, a_base, i); };
     auto read_b = [&](const char *st, int j) { return read_frag<C, C::BKN>(st + C::kA, b_base, j); };
-    auto fetch = [&](int t, char *st) {
-        a.fetch(t, st, wave, lane);
-        b.fetch(t, st + C::kA, wave, lane);
+    constexpr int NA = Loader<C, C::AKN, BM>::kLoads, NB = Loader<C, C::BKN, BN>::kLoads;
+    // Loads from..to-1 of a slab's NA + NB, from its two resources.
+    auto load = [&](const rsrc_t &ra, const rsrc_t &rb, char *st, int from, int to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int l = from; l < to; ++l) {
+            if (l < NB) b.load(rb, st + C::kA, wave, l);
+            else a.load(ra, st, wave, l - NB);
+        }
+    };
+    auto fetch = [&](int t, char *st) __attribute__((always_inline)) {
+        if constexpr (C::DMA) {
+            load(a.source(t), b.source(t), st, 0, NA + NB);
+        } else {
+            a.hold(t, wave, lane);
+            b.hold(t, wave, lane);
+        }
     };
     auto stash = [&](char *st) {
         a.stash(st, wave, lane);
         b.stash(st + C::kA, wave, lane);
     };
 
+    // fp8: the partial tile of one product is added while the next one is
+    // multiplied, half of it behind each matrix instruction, so that a wave
+    // keeps the matrix core busy by itself.  The last product's of a slab is
+    // added by the next slab (kCarry: an even number of products, so that it is
+    // always in part[1]); s_due is the scale it takes.
+    constexpr int kProducts = FM * FN;
+    constexpr bool kCarry = kProducts % 2 == 0;
+    f32x16 part[2] = {};
+    float s_due = 0.0f;
+    // Half of the partial tile of product n (modulo their number).
+    auto add = [&](int n, int half) __attribute__((always_inline)) {
+        if constexpr (FP8) {
+            const int m = (n + kProducts) % kProducts;
+#pragma unroll
+            for (int e = 8 * half; e < 8 * half + 8; ++e)
+                acc[m / FN][m % FN][e] = fmaf(part[m & 1][e], s_due, acc[m / FN][m % FN][e]);
+        }
+    };
     // Products of slab t, whose fragments (B's, and A's first) are in
     // registers, from stage `cur`; meanwhile slab t + 1 lands in `next`, whose
     // first fragments are read at the end, and slab t + 2 is sent for.
-    // `first`: the set that holds A's first fragment; `set`: that of the scales.
-    auto slab = [&](int t, char *cur, char *next, int first, int set) __attribute__((always_inline)) {
+    // `first`: the set that holds A's first fragment; `scales`: the slab's.
+    //
+    // With four steps a slab (kSpread) the loads go out one between two matrix
+    // instructions, half of them behind the barrier and the rest in the next
+    // slab's first step: sent in a row they hold up the matrix instructions
+    // behind them (8192^3 fp8: 500 us; 480 spread over the last step, 465 so).
+    // Tiles of fewer steps wait for memory rather than for the matrix cores,
+    // and send them at once.
+    constexpr bool kSpread = C::DMA && FM == 4;
+    constexpr int kFirst = (NA + NB) / 2, kRest = NA + NB - kFirst;
+    auto slab = [&](int t, char *cur, char *next, int first, float *scales) __attribute__((always_inline)) {
         // Addresses are made again from these in every slab: kept across the loop they would
         // take more registers than there are.
         asm volatile("" : "+v"(a_base), "+v"(b_base), "+v"(a.off), "+v"(b.off));
+        rsrc_t ra, rb;
+        if (kSpread) {
+            ra = a.source(t + 1);
+            rb = b.source(t + 1);
+        }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int s = (first + i) & 1;
+            const float s_ab = scale_of(scales, i);
             if (i + 1 < FM) {
                 fa[s ^ 1] = read_a(cur, i + 1);
             } else {
@@ -355,54 +415,66 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
                 __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
                 __builtin_amdgcn_s_barrier();
                 fa[s ^ 1] = read_a(next, 0);
-                fetch(t + 2, cur);
-            }
-            const float s_ab = FP8 ? sc_a[set][i] * sc_b[set] : 0.0f;
-            // A partial tile is added while the next one is multiplied; with 128
-            // accumulators there are registers for one only, and the SIMD's
-            // other wave has the matrix core meanwhile.
-            constexpr int kParts = FM * FN >= 99 ? 1 : FN;
-            f32x16 part[kParts];
-            auto add = [&](int j) __attribute__((always_inline)) {
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(part[j % kParts][e], s_ab, acc[i][j][e]);
+                load_scales(t + 2, scales);
+                if constexpr (kSpread) {
+                    ra = a.source(t + 2);
+                    rb = b.source(t + 2);
+                } else {
+                    fetch(t + 2, cur);
                 }
+            }
+            // The loads that go out in gap g (0 .. 2 * FN - 1) of this step.
+            auto send = [&](int g) __attribute__((always_inline)) {
+                if (kSpread && i + 1 == FM) load(ra, rb, cur, g * kFirst / (2 * FN), (g + 1) * kFirst / (2 * FN));
+                if (kSpread && i == 0)
+                    load(ra, rb, next, kFirst + g * kRest / (2 * FN), kFirst + (g + 1) * kRest / (2 * FN));
             };
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                if constexpr (FP8) part[j % kParts] = product_fp8(fa[s], fb[j]);
-                else acc[i][j] = product_bf16(fa[s], fb[j], acc[i][j]);
+                const int n = i * FN + j;
+                if constexpr (FP8) part[n & 1] = product_fp8(fa[s], fb[j], 0, f32x16{});
+                else acc[i][j] = product_bf16(fa[s], fb[j], 0, acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (kCarry || n > 0) add(n - 1, 0);
+                send(2 * j);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (FP8) part[n & 1] = product_fp8(fa[s], fb[j], 1, part[n & 1]);
+                else acc[i][j] = product_bf16(fa[s], fb[j], 1, acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
                 if (i + 1 == FM) fb[j] = read_b(next, j);
-                if (kParts == 1 && FN > 1) add(j);
-                else if (j > 0) add(j - 1);
+                if (kCarry || n > 0) add(n - 1, 1);
+                send(2 * j + 1);
+                s_due = s_ab;
             }
-            if (kParts > 1 || FN == 1) add(FN - 1);
-            if (i + 1 == FM) scales(t + 2, set);
+            if (!kCarry && i + 1 == FM) {
+                add(-1, 0);
+                add(-1, 1);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (len > 0) {
-        scales(0, 0);
-        scales(1, 1);
+        load_scales(0, scale0);
         fetch(0, st0);
         stash(st0);
-        fetch(1, st1);
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(C::DMA ? a.kLoads + b.kLoads : 63));
+        load_scales(1, scale1);
+        if (kSpread) load(a.source(1), b.source(1), st1, 0, kFirst);
+        else fetch(1, st1);
+        // Slab 0 has landed when only slab 1's loads are left.
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0)));
         __builtin_amdgcn_s_barrier();
         fa[0] = read_a(st0, 0);
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[j] = read_b(st0, j);
         int t = 0;
         for (; t + 1 < nk; t += 2) {
-            slab(t, st0, st1, 0, 0);
-            slab(t + 1, st1, st0, FM & 1, 1);
+            slab(t, st0, st1, 0, scale0);
+            slab(t + 1, st1, st0, FM & 1, scale1);
         }
-        if (t < nk) slab(t, st0, st1, 0, 0);
+        if (t < nk) slab(t, st0, st1, 0, scale0);
         if (cut) {
-            // Slab nk ends K inside a chunk.  It has landed (slab 0: the wait above), every
+            // Slab nk ends K.  It has landed (slab 0: the wait above), every
             // wave has read what it will of it, and it is read again.
             char *cur = (nk & 1) ? st1 : st0, *next = (nk & 1) ? st0 : st1;
             const int tail = (int)(((int64_t)len - (int64_t)nk * C::BK) * C::esz);
@@ -415,12 +487,11 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             fa[0] = read_a(cur, 0);
 #pragma unroll
             for (int j = 0; j < FN; ++j) fb[j] = read_b(cur, j);
-            if (nk & 1) {
-#pragma unroll
-                for (int i = 0; i < FM; ++i) sc_a[0][i] = sc_a[1][i];
-                sc_b[0] = sc_b[1];
-            }
-            slab(nk, cur, next, 0, 0);
+            slab(nk, cur, next, 0, (nk & 1) ? scale1 : scale0);
+        }
+        if (kCarry) {
+            add(-1, 0);
+            add(-1, 1);
         }
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
         __builtin_amdgcn_s_barrier();
@@ -436,7 +507,11 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     const bool bf16_out = !WGRAD && p.out_type == GEMM_OUT_BF16;
     const uintptr_t at = bf16_out ? reinterpret_cast<uintptr_t>(oh) & 7 : reinterpret_cast<uintptr_t>(of) & 15;
     const bool vec = at == 0 && p.ldo % 4 == 0;
-    const int cc = lane % kChunks;
+    // The lane again, opaque: what is made of it stays out of the loop's registers.
+    int elane = threadIdx.x & 63;
+    asm volatile("" : "+v"(elane));
+    const int el32 = elane & 31;
+    const int cc = elane % kChunks;
     const int col = wn * 32 * FN + 4 * cc;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -444,14 +519,14 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int c = (8 * j + 2 * g + (lane >> 5)) ^ (l32 & (kChunks - 1));
-                *reinterpret_cast<f32x4 *>(piece + l32 * (kChunks * 16) + 16 * c) =
+                const int c = (8 * j + 2 * g + (elane >> 5)) ^ (el32 & (kChunks - 1));
+                *reinterpret_cast<f32x4 *>(piece + el32 * (kChunks * 16) + 16 * c) =
                     f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
             }
         constexpr int kRows = 64 / kChunks;          // rows an instruction takes
 #pragma unroll
         for (int r0 = 0; r0 < 32; r0 += kRows) {
-            const int r = r0 + lane / kChunks;
+            const int r = r0 + elane / kChunks;
             f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (kChunks * 16) + 16 * (cc ^ (r & (kChunks - 1))));
             const int row = (wm * FM + i) * 32 + r;
             if (row >= out_rows || col >= out_cols) continue;
