@@ -101,6 +101,9 @@ gemm_status run(const Product &c, gemm_stream_t stream) {
     if (!tiles) return launched(gemm::launch_grouped_general(c.dtype, c.op_b, p, s));
     if (c.M == 1) p.lda = ceil_div(c.K * sz, 16) * 16 / sz;          // the stride of a single row is not used
     const bool dma = rows_on16(c.A, p.lda, sz) && rows_on16(c.B, c.ldb, sz) && c.stride_b * sz % 16 == 0;
+    if (dma)
+        if (const int rows = gemm::skinny_rows(c.dtype, c.op_b, p))
+            return launched(gemm::launch_grouped_skinny(c.dtype, rows, p, s));
     return launched(c.dtype == GEMM_DTYPE_FP8F32 ? gemm::launch_grouped_fp8(c.op_b, dma, p, s)
                                                  : gemm::launch_grouped_bf16(c.op_b, dma, p, s));
 }

@@ -8,16 +8,23 @@ hipError_t launch_grouped_bf16(int32_t op_b, bool dma, const GroupedParams &p, h
     return launch_typed<GEMM_DTYPE_BF16F32>(op_b, dma, p, stream);
 }
 
-// Weight gradients: both operands are walked down their rows.
+// Weight gradients: both operands are walked down their rows.  Results are
+// fp32, so a tile's store takes twice the time.
 hipError_t launch_wgrad_bf16(bool dma, const GroupedParams &p, hipStream_t s) {
-    auto tiles = [&](int64_t b) { return ((p.N + b - 1) / b) * ((p.K + b - 1) / b) * p.groups; };
     constexpr int DT = GEMM_DTYPE_BF16F32;
-    if (tiles(128) < 256)
-        return dma ? launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, true>>(p, s)
-                   : launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, false>>(p, s);
-    if (!dma) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, false>>(p, s);
-    return tiles(256) >= 256 ? launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s)
-                             : launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, true>>(p, s);
+    // The outputs of all groups together, each as deep as a group has rows.
+    const double slabs = std::ceil((double)p.M / p.groups / 64);
+    switch (tile_size((double)p.N * p.groups, p.K, slabs, p.groups, dma ? kTile256 : kTile128, 2.0)) {
+        case kTile256:
+        case kTileWide:
+            if (dma) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s);
+        case kTile128:
+            return dma ? launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, true>>(p, s)
+                       : launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, false>>(p, s);
+        default:
+            return dma ? launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, true>>(p, s)
+                       : launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, false>>(p, s);
+    }
 }
 
 }  // namespace gemm

@@ -37,6 +37,9 @@
 // loaded so that it ends with the row and shifted into place.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "gemm_grouped.hpp"
 
 #if defined(__HIPCC__)
@@ -56,10 +59,11 @@ struct __attribute__((packed, aligned(1))) Bytes16 {
     u32x4 v;
 };
 
-template <int DT_, int FM_, int FN_, int WM_, int WN_, bool AKN_, bool BKN_, bool DMA_>
+template <int DT_, int FM_, int FN_, int WM_, int WN_, bool AKN_, bool BKN_, bool DMA_, int NS_ = 2>
 struct TileConfig {
     static constexpr int DT = DT_, FM = FM_, FN = FN_, WM = WM_, WN = WN_;
     static constexpr bool AKN = AKN_, BKN = BKN_, DMA = DMA_;
+    static constexpr int NS = NS_;                    // LDS stages
     static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
     static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : 2;
     static constexpr int BK = kSlab / esz;            // k a slab
@@ -242,7 +246,12 @@ __global__ void __launch_bounds__(64 * C::NW, 2)
 grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     constexpr int FM = C::FM, FN = C::FN, NW = C::NW, BM = C::BM, BN = C::BN;
     constexpr bool FP8 = C::DT == GEMM_DTYPE_FP8F32, WGRAD = C::AKN;
-    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
+    constexpr int NS = C::NS;
+    static_assert(NS == 2 || (NS == 3 && FM % 2 == 0 && C::DMA), "");
+    // One array a stage: the compiler can then tell that a read of one does not depend on
+    // loads still landing in another.
+    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage], st2[NS > 2 ? C::kStage : 16];
+    auto stage = [&](int i) __attribute__((always_inline)) -> char * { return i == 0 ? st0 : i == 1 ? st1 : st2; };
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -296,16 +305,17 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     const int nk = cut ? len / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
 
     const int l32 = lane & 31;
-    // Scales of the block that slab t is go to LDS as the slab does (of even
-    // slabs to one set, of odd ones to the other): wave w < kScaleA loads those
+    // Scales of the block that slab t is go to LDS as the slab does, into its
+    // stage's set: wave w < kScaleA loads those
     // of 64 rows, the next wave those of the tile's column blocks, the others
     // nothing; five loads a wave and slab from global memory instead cost a
     // tenth of the whole call.
     constexpr int kScaleA = (BM + 63) / 64;
     static_assert(!FP8 || kScaleA < NW, "a wave for each 64 rows and one for the columns");
-    // One array a set, as for the stages: the compiler can then tell that a read of one does
-    // not depend on loads still landing in the other.
-    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1];
+    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1], scale2[FP8 && NS > 2 ? NW * 64 : 1];
+    auto scale_set = [&](int i) __attribute__((always_inline)) -> float * {
+        return i == 0 ? scale0 : i == 1 ? scale1 : scale2;
+    };
     const float *sc_base = nullptr;
     int64_t sc_step = 0;
     uint32_t sc_bytes = 0, sc_off = 0;
@@ -393,14 +403,15 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     // behind them (8192^3 fp8: 500 us; 480 spread over the last step, 465 so).
     // Tiles of fewer steps wait for memory rather than for the matrix cores,
     // and send them at once.
-    constexpr bool kSpread = C::DMA && FM == 4;
-    constexpr int kFirst = (NA + NB) / 2, kRest = NA + NB - kFirst;
+    constexpr bool kSpread = C::DMA && NW == 8;
+    constexpr int kFirst = NS == 2 ? (NA + NB) / 2 : NA + NB, kRest = NA + NB - kFirst;
+    constexpr int kSlabLoads = NA + NB + (FP8 ? 1 : 0);
     auto slab = [&](int t, char *cur, char *next, int first, float *scales) __attribute__((always_inline)) {
         // Addresses are made again from these in every slab: kept across the loop they would
         // take more registers than there are.
         asm volatile("" : "+v"(a_base), "+v"(b_base), "+v"(a.off), "+v"(b.off));
         rsrc_t ra, rb;
-        if (kSpread) {
+        if (kSpread && kRest > 0) {
             ra = a.source(t + 1);
             rb = b.source(t + 1);
         }
@@ -412,15 +423,16 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
                 fa[s ^ 1] = read_a(cur, i + 1);
             } else {
                 stash(next);
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+                // Slab t + 1 has landed; of three stages, slab t + 2's loads may be under way.
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * kSlabLoads));
                 __builtin_amdgcn_s_barrier();
                 fa[s ^ 1] = read_a(next, 0);
-                load_scales(t + 2, scales);
+                load_scales(t + NS, scales);
                 if constexpr (kSpread) {
-                    ra = a.source(t + 2);
-                    rb = b.source(t + 2);
+                    ra = a.source(t + NS);
+                    rb = b.source(t + NS);
                 } else {
-                    fetch(t + 2, cur);
+                    fetch(t + NS, cur);
                 }
             }
             // The loads that go out in gap g (0 .. 2 * FN - 1) of this step.
@@ -458,25 +470,34 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         load_scales(0, scale0);
         fetch(0, st0);
         stash(st0);
-        load_scales(1, scale1);
-        if (kSpread) load(a.source(1), b.source(1), st1, 0, kFirst);
-        else fetch(1, st1);
-        // Slab 0 has landed when only slab 1's loads are left.
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0)));
+#pragma unroll
+        for (int i = 1; i < NS; ++i) {
+            load_scales(i, scale_set(i));
+            if (kSpread) load(a.source(i), b.source(i), stage(i), 0, kFirst);
+            else fetch(i, stage(i));
+        }
+        // Slab 0 has landed when only the others' loads are left.
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 1) * ((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0))));
         __builtin_amdgcn_s_barrier();
         fa[0] = read_a(st0, 0);
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[j] = read_b(st0, j);
         int t = 0;
-        for (; t + 1 < nk; t += 2) {
-            slab(t, st0, st1, 0, scale0);
-            slab(t + 1, st1, st0, FM & 1, scale1);
+        // Whole turns of the stages as straight-line code, then the rest.
+        constexpr int kTurn = FM % 2 == 0 ? NS : 2;
+        for (; t + kTurn <= nk; t += kTurn) {
+#pragma unroll
+            for (int u = 0; u < kTurn; ++u)
+                slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u));
         }
-        if (t < nk) slab(t, st0, st1, 0, scale0);
+#pragma unroll
+        for (int u = 0; u < kTurn - 1; ++u)
+            if (t + u < nk) slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u));
         if (cut) {
             // Slab nk ends K.  It has landed (slab 0: the wait above), every
             // wave has read what it will of it, and it is read again.
-            char *cur = (nk & 1) ? st1 : st0, *next = (nk & 1) ? st0 : st1;
+            const int at = nk % NS;
+            char *cur = stage(at), *next = stage((at + 1) % NS);
             const int tail = (int)(((int64_t)len - (int64_t)nk * C::BK) * C::esz);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
             __builtin_amdgcn_s_barrier();
@@ -487,7 +508,7 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             fa[0] = read_a(cur, 0);
 #pragma unroll
             for (int j = 0; j < FN; ++j) fb[j] = read_b(cur, j);
-            slab(nk, cur, next, 0, (nk & 1) ? scale1 : scale0);
+            slab(nk, cur, next, 0, scale_set(at));
         }
         if (kCarry) {
             add(-1, 0);
@@ -562,6 +583,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     }
 }
 
+constexpr int kComputeUnits = 256;
+
 template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStream_t stream) {
     GroupedParams args = p;
     int tiles_m, tiles_n;
@@ -580,26 +603,59 @@ template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStr
                            stream);
 }
 
-// 256 x 256 (eight waves), 128 x 128, 64 x 128 and 32 x 128 (four waves).
-enum TileSize { kTile256, kTile128, kTile64, kTile32 };
+// Tiles and how long they take: 256 x 256 and 128 x 256 (eight waves, the
+// latter on three stages), 128 x 128, 64 x 128 and 32 x 128 (four waves).
+enum TileSize { kTile256, kTileWide, kTile128, kTile64, kTile32 };
 
-// Few rows a group: the tile that holds them, so that little of it is empty.
-// Otherwise the largest tile that still gives every compute unit one.
-inline TileSize tile_size(const GroupedParams &p, bool dma) {
-    const int64_t groups = p.ends != nullptr ? p.groups : 1, rows = p.M / (groups > 0 ? groups : 1);
-    auto tiles = [&](int bm, int bn) {
-        return most_row_tiles(p.M, p.groups, bm, p.ends != nullptr) * ((p.N + bn - 1) / bn);
-    };
-    if (rows <= 32) return kTile32;
-    if (rows <= 64 || tiles(128, 128) < 256) return kTile64;
-    return dma && tiles(256, 256) >= 256 ? kTile256 : kTile128;
+struct TileCost {
+    int bm, bn;
+    // us: a slab's and a tile's share of a busy compute unit's time, and a slab of a lone
+    // workgroup (measured at 64 .. 8192 rows of K = 777 .. 16384, fp8 and bf16 alike since a slab
+    // has the same bytes and matrix cycles).
+    double slab, tile, alone;
+};
+constexpr TileCost kTileCosts[] = {
+    {256, 256, 1.6, 8.0, 1.2}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.78}, {64, 128, 0.40, 2.5, 0.5},
+    {32, 128, 0.33, 1.2, 0.45}};
+
+// The tile of the least time over `rows` rows of an output of `cols` columns,
+// `slabs` slabs deep, in `groups` groups: large ones move the fewest bytes a
+// product (2048 x 4096 x 4096 fp8: 42 us in 128 x 256, 50 in 128 x 128, 57
+// in 256 x 256, which leaves half of the compute units idle; 8192^3: 560,
+// 600 and 520 us; 16 groups of 8192 x 4096 x 4096: 225, 235 and 195 us; 64
+// rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128).  Groups are taken to be
+// alike, with half an empty tile each at their ends.
+// `first`: the largest to consider.
+inline TileSize tile_size(double rows, double cols, double slabs, double groups, TileSize first,
+                          double tile_factor = 1.0) {
+    TileSize best = kTile32;
+    double least = 0.0;
+    for (int i = first; i <= kTile32; ++i) {
+        const TileCost &c = kTileCosts[i];
+        const double each = rows / groups / c.bm + 0.5;
+        const double tiles = (groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm)) * std::ceil(cols / c.bn);
+        const double turns = std::ceil(tiles / kComputeUnits);
+        const double t = std::max(turns * (slabs * c.slab + c.tile * tile_factor), slabs * c.alone + 6.0);
+        if (i == first || t < least) {
+            least = t;
+            best = static_cast<TileSize>(i);
+        }
+    }
+    return best;
 }
 
 template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParams &p, hipStream_t s) {
-    switch (tile_size(p, DMA)) {
+    const double slabs = std::ceil((double)p.K * (DT == GEMM_DTYPE_FP8F32 ? 1 : 2) / kSlab);
+    const double groups = p.ends != nullptr ? std::max(1, std::min(p.groups, p.M)) : 1;
+    // Staging registers leave room for fewer accumulators, partial tiles for fewer still.
+    constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32;
+    switch (tile_size(p.M, p.N, slabs, groups, DMA ? kTile256 : FP8 ? kTile64 : kTile128)) {
         case kTile256:
             if constexpr (DMA) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
-        case kTile128: return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
+        case kTileWide:
+            if constexpr (DMA) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
+        case kTile128:
+            if constexpr (DMA || !FP8) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
         case kTile64: return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
         default: return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA>>(p, s);
     }
