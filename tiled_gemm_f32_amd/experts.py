@@ -81,12 +81,11 @@ def _blocks(n: int) -> int:
     return -(-n // GEMM_SCALE_BLOCK)
 
 
-def _codes(rows: int, cols: int, device):
-    """rows x cols codes whose rows start on 16 bytes, which the matrix-core paths ask for."""
+def _new(rows: int, cols: int, dtype, device, unit: int = 1):
+    """(tensor, leading dimension): an uninitialised rows x cols matrix whose rows start on multiples of `unit`."""
     import torch
-    if cols % 16 == 0:
-        return torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
-    return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+    ld = max(-(-cols // unit) * unit, 1)
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device), ld
 
 
 def _call(name: str, device: int, stream, made, fn, *args):
@@ -124,15 +123,19 @@ def quantize(x, block_rows: int = 1, out=None, scales=None, stream=None):
     M, K = x.shape
     made = []
     if out is None:
-        out = _codes(M, K, x.device)
+        out, ldq = _new(M, K, torch.float8_e4m3fn, x.device, 16)
         made.append(out)
+    else:
+        _check(out, "out", device, (M, K), torch.float8_e4m3fn)
+        ldq = _ld(out, "out")
     if scales is None:
-        scales = torch.empty((-(-M // block_rows), _blocks(K)), dtype=torch.float32, device=x.device)
+        scales, lds = _new(-(-M // block_rows), _blocks(K), torch.float32, x.device)
         made.append(scales)
-    _check(out, "out", device, (M, K), torch.float8_e4m3fn)
-    _check(scales, "scales", device, (-(-M // block_rows), _blocks(K)), torch.float32)
+    else:
+        _check(scales, "scales", device, (-(-M // block_rows), _blocks(K)), torch.float32)
+        lds = _ld(scales, "scales")
     _call("quantize", device, stream, made, gemm_quantize, dt, block_rows, M, K, x.data_ptr(), _ld(x, "x"),
-          out.data_ptr(), _ld(out, "out"), scales.data_ptr(), _ld(scales, "scales"))
+          out.data_ptr(), ldq, scales.data_ptr(), lds)
     return out, scales
 
 
@@ -155,33 +158,39 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
     if N > 1 and weight.stride(0) != 1:
         raise ValueError("weight must be contiguous")
     made = []
+    r_ptr = s_ptr = c_ptr = ldr = ld_sum = ld_scales = 0
     if residual is not None:
         _check(residual, "residual", device, (M, N), x.dtype)
-        if summed is None:
-            summed = torch.empty((M, N), dtype=x.dtype, device=x.device)
-            made.append(summed)
+        r_ptr, ldr = residual.data_ptr(), _ld(residual, "residual")
     if summed is not None:
         _check(summed, "summed", device, (M, N), x.dtype)
-    if out is not None and out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    kind = _out_type(out.dtype if out is not None else out_dtype or x.dtype, "out")
-    if out is None:
-        out = _codes(M, N, x.device) if kind == GEMM_OUT_FP8 else torch.empty((M, N), dtype=out_dtype or x.dtype,
-                                                                              device=x.device)
+        s_ptr, ld_sum = summed.data_ptr(), _ld(summed, "summed")
+    elif residual is not None:
+        summed, ld_sum = _new(M, N, x.dtype, x.device)
+        made.append(summed)
+        s_ptr = summed.data_ptr()
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        kind = _out_type(out.dtype, "out")
+        _check(out, "out", device, (M, N))
+        ldo = _ld(out, "out")
+    else:
+        kind = _out_type(out_dtype or x.dtype, "out")
+        out, ldo = _new(M, N, out_dtype or x.dtype, x.device, 16 if kind == GEMM_OUT_FP8 else 1)
         made.append(out)
-    _check(out, "out", device, (M, N))
     if kind == GEMM_OUT_FP8:
         if scales is None:
-            scales = torch.empty((M, _blocks(N)), dtype=torch.float32, device=x.device)
+            scales, ld_scales = _new(M, _blocks(N), torch.float32, x.device)
             made.append(scales)
-        _check(scales, "scales", device, (M, _blocks(N)), torch.float32)
+        else:
+            _check(scales, "scales", device, (M, _blocks(N)), torch.float32)
+            ld_scales = _ld(scales, "scales")
+        c_ptr = scales.data_ptr()
     elif scales is not None:
         raise ValueError("scales go with a float8_e4m3fn output")
-    _call("rms_norm", device, stream, made, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"),
-          residual.data_ptr() if residual is not None else 0, _ld(residual, "residual") if residual is not None else 0,
-          weight.data_ptr(), float(eps), summed.data_ptr() if summed is not None else 0,
-          _ld(summed, "summed") if summed is not None else 0, kind, out.data_ptr(), _ld(out, "out"),
-          scales.data_ptr() if scales is not None else 0, _ld(scales, "scales") if scales is not None else 0)
+    _call("rms_norm", device, stream, made, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"), r_ptr, ldr,
+          weight.data_ptr(), float(eps), s_ptr, ld_sum, kind, out.data_ptr(), ldo, c_ptr, ld_scales)
     return out, summed if summed is not None else x, scales
 
 
@@ -206,20 +215,23 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
         _check(dsum, "dsum", device, (M, N), dy.dtype)
     made = []
     if dx is None:
-        dx = torch.empty((M, N), dtype=dy.dtype, device=dy.device)
+        dx, lddx = _new(M, N, dy.dtype, dy.device)
         made.append(dx)
-    _check(dx, "dx", device, (M, N), dy.dtype)
-    dweight = ws = None
-    need = 0
+    else:
+        _check(dx, "dx", device, (M, N), dy.dtype)
+        lddx = _ld(dx, "dx")
+    dweight = None
+    dw_ptr = ws_ptr = need = 0
     if want_dweight:
         need = gemm_rms_norm_workspace_size(M, N)
-        dweight = torch.empty(N, dtype=torch.float32, device=dy.device)
-        ws = torch.empty(max(need, 4), dtype=torch.uint8, device=dy.device)
+        dweight = torch.empty_strided((N,), (1,), dtype=torch.float32, device=dy.device)
+        ws = torch.empty_strided((max(need, 4),), (1,), dtype=torch.uint8, device=dy.device)
         made += [dweight, ws]
+        dw_ptr, ws_ptr = dweight.data_ptr(), ws.data_ptr()
     _call("rms_norm_backward", device, stream, made, gemm_rms_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
           summed.data_ptr(), _ld(summed, "summed"), weight.data_ptr(), float(eps),
-          dsum.data_ptr() if dsum is not None else 0, _ld(dsum, "dsum") if dsum is not None else 0, dx.data_ptr(),
-          _ld(dx, "dx"), dweight.data_ptr() if dweight is not None else 0, ws.data_ptr() if ws is not None else 0, need)
+          dsum.data_ptr() if dsum is not None else 0, _ld(dsum, "dsum") if dsum is not None else 0, dx.data_ptr(), lddx,
+          dw_ptr, ws_ptr, need)
     return dx, dweight
 
 
@@ -238,7 +250,8 @@ def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int, d
     for t, what in ((a_scales, "a_scales"), (b_scales, "b_scales")):
         if t is None:
             raise ValueError(f"float8_e4m3fn operands need {what}")
-        _check(t, what, device, t.shape, torch.float32)
+        if t.get_device() != device or t.dtype is not torch.float32:
+            _check(t, what, device, t.shape, torch.float32)
     a_row, a_block = _strides(a_scales, 0, (M, _blocks(K)), "a_scales")
     lead = B.dim() - 2
     shape = tuple(B.shape[:lead]) + (_blocks(B.shape[-2]), _blocks(B.shape[-1]))
@@ -249,17 +262,18 @@ def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int, d
 
 
 def _product_out(M: int, N: int, out, out_dtype, default, like, device: int, made):
-    import torch
+    """(out, its leading dimension, its type) of a product."""
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     kind = _out_type(out.dtype if out is not None else out_dtype or default, "out")
     if kind == GEMM_OUT_FP8:
         raise TypeError("out must be float32 or bfloat16")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or default, device=like.device)
-        made.append(out)
-    _check(out, "out", device, (M, N))
-    return out, kind
+    if out is not None:
+        _check(out, "out", device, (M, N))
+        return out, _ld(out, "out"), kind
+    out, ldo = _new(M, N, out_dtype or default, like.device)
+    made.append(out)
+    return out, ldo, kind
 
 
 def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, out=None, out_dtype=None, stream=None):
@@ -282,9 +296,9 @@ def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, ou
         raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, op_b={op_b} {tuple(B.shape)}")
     sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K, device)
     made = []
-    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device, made)
+    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device, made)
     _call("block_gemm", device, stream, made, gemm_block_scaled, GEMM_OP_T if op_b == "T" else GEMM_OP_N, M, N, K,
-          float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), sc, kind, out.data_ptr(), _ld(out, "out"))
+          float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), sc, kind, out.data_ptr(), ldo)
     return out
 
 
@@ -325,10 +339,10 @@ def grouped_gemm(A, B, ends, a_scales=None, b_scales=None, op_b: str = "T", alph
     elif a_scales is not None or b_scales is not None:
         raise ValueError("scales go with float8_e4m3fn operands")
     made = []
-    out, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A, device, made)
+    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A, device, made)
     _call("grouped_gemm", device, stream, made, gemm_grouped, dt, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
           ends.data_ptr(), M, N, K, float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
-          B.stride(0) if groups > 1 else 0, sc, kind, out.data_ptr(), _ld(out, "out"))
+          B.stride(0) if groups > 1 else 0, sc, kind, out.data_ptr(), ldo)
     return out
 
 
