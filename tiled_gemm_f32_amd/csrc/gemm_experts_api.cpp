@@ -95,12 +95,13 @@ gemm_status run(const Product &c, gemm_stream_t stream) {
     if (c.sc != nullptr) p.sc = *c.sc;
     // A row's bytes must hold one 16-byte load, whatever their alignment.
     const int64_t sz = (int64_t)esz;
-    const bool tiles = c.dtype != GEMM_DTYPE_F32 && c.K * sz >= 16 && b_len * sz >= 16 && c.lda * sz < kMaxTileRow &&
+    const bool tiles = c.K * sz >= 16 && b_len * sz >= 16 && c.lda * sz < kMaxTileRow &&
                        c.ldb * sz < kMaxTileRow && (c.sc == nullptr || (c.sc->a_row < kMaxTileRow / 4 && c.sc->b_n < kMaxTileRow));
     const auto s = static_cast<hipStream_t>(stream);
     if (!tiles) return launched(gemm::launch_grouped_general(c.dtype, c.op_b, p, s));
     if (c.M == 1) p.lda = ceil_div(c.K * sz, 16) * 16 / sz;          // the stride of a single row is not used
     const bool dma = rows_on16(c.A, p.lda, sz) && rows_on16(c.B, c.ldb, sz) && c.stride_b * sz % 16 == 0;
+    if (c.dtype == GEMM_DTYPE_F32) return launched(gemm::launch_grouped_f32(c.op_b, dma, p, s));
     if (dma)
         if (const int rows = gemm::skinny_rows(c.dtype, c.op_b, p))
             return launched(gemm::launch_grouped_skinny(c.dtype, rows, p, s));
@@ -167,9 +168,10 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
     p.beta = beta;
     const int64_t sz = (int64_t)esz;
     const auto s = static_cast<hipStream_t>(stream);
-    if (dtype == GEMM_DTYPE_F32 || N * sz < 16 || K * sz < 16 || lddy * sz >= kMaxTileRow || ldx * sz >= kMaxTileRow)
+    if (N * sz < 16 || K * sz < 16 || lddy * sz >= kMaxTileRow || ldx * sz >= kMaxTileRow)
         return launched(gemm::launch_wgrad_general(dtype, p, s));
-    return launched(gemm::launch_wgrad_bf16(rows_on16(dY, lddy, sz) && rows_on16(X, ldx, sz), p, s));
+    const bool dma = rows_on16(dY, lddy, sz) && rows_on16(X, ldx, sz);
+    return launched(dtype == GEMM_DTYPE_F32 ? gemm::launch_wgrad_f32(dma, p, s) : gemm::launch_wgrad_bf16(dma, p, s));
 }
 
 GEMM_API gemm_status gemm_quantize(int32_t dtype, int32_t block_rows, int64_t M, int64_t K, const void *X, int64_t ldx,

@@ -145,11 +145,13 @@ __device__ __forceinline__ void find_group(const GroupedParams &p, int g, int &l
 // start on 16 bytes.
 hipError_t launch_grouped_fp8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_bf16(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_grouped_f32(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 // Few rows (on average 64 a group at most) and weights stored N x K, rows on
 // 16 bytes: the rows of the tile that suits, or 0 for calls that are not its.
 int skinny_rows(int32_t dtype, int32_t op_b, const GroupedParams &p);
 hipError_t launch_grouped_skinny(int32_t dtype, int rows, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_bf16(bool dma, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_wgrad_f32(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_general(int32_t dtype, const GroupedParams &p, hipStream_t stream);
 

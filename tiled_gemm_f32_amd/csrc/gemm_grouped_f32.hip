@@ -1,0 +1,15 @@
+// Grouped fp32 products and their weight gradients on the tiles of
+// gemm_grouped_tile.hpp.
+#include "gemm_grouped_tile.hpp"
+
+namespace gemm {
+
+hipError_t launch_grouped_f32(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream) {
+    return launch_typed<GEMM_DTYPE_F32>(op_b, dma, p, stream);
+}
+
+hipError_t launch_wgrad_f32(bool dma, const GroupedParams &p, hipStream_t stream) {
+    return launch_wgrad<GEMM_DTYPE_F32>(dma, p, stream);
+}
+
+}  // namespace gemm

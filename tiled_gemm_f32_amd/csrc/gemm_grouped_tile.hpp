@@ -1,5 +1,5 @@
-// Tile kernel of the grouped and block-scaled products, for bf16 and fp8
-// operands: instantiated in gemm_grouped_bf16.hip and gemm_grouped_fp8.hip.
+// Tile kernel of the grouped and block-scaled products: instantiated in
+// gemm_grouped_f32.hip, gemm_grouped_bf16.hip and gemm_grouped_fp8.hip.
 //
 // A workgroup makes a tile of BM x BN outputs of one group, walking k in
 // slabs of 128 bytes a row (64 bf16 or 128 fp8 values: for fp8 exactly one
@@ -28,13 +28,15 @@
 //     k row r at c ^ 4*((r >> 1) & 1), read with ds_read_b64_tr_b16.
 //   fp8 stored the other way: [128-column block][128 k][8 chunks], chunk c of
 //     k row r at c ^ (r & 7), read with ds_read_b64_tr_b8.
+//   fp32 stored the other way: [32-column block][32 k][8 chunks], read a value a
+//     lane (a fragment pair's 16 instructions take 1024 cycles, its reads some
+//     100).
 //
 // DMA: operands whose rows start on 16 bytes come by direct-to-LDS buffer
 // loads.  Rows past the ends fall outside the buffer resource and read as
 // zero; where K ends inside a slab, what the loads brought past it is zeroed
-// in LDS before it is read.  Otherwise (REG) chunks go
-// through registers with unaligned 16-byte loads, the last one of a row
-// loaded so that it ends with the row and shifted into place.
+// in LDS before it is read.  Otherwise (REG) chunks go through registers with
+// unaligned 16-byte loads, and the last slab is put in order in LDS.
 #pragma once
 
 #include <algorithm>
@@ -65,8 +67,11 @@ struct TileConfig {
     static constexpr bool AKN = AKN_, BKN = BKN_, DMA = DMA_;
     static constexpr int NS = NS_;                    // LDS stages
     static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
-    static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : 2;
+    static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : DT == GEMM_DTYPE_BF16F32 ? 2 : 4;
     static constexpr int BK = kSlab / esz;            // k a slab
+    // REG: slabs under way in registers.  Two where there is room: a small tile's products of one
+    // slab do not cover a load.
+    static constexpr int kSets = FM == 1 ? 2 : 1;
     static constexpr int kA = BM * kSlab, kB = BN * kSlab, kStage = kA + kB;
 };
 
@@ -77,18 +82,19 @@ struct Loader {
     static constexpr int esz = C::esz;
     static constexpr int kLoads = ROWS * 8 / (64 * C::NW);    // 16-byte chunks a thread and slab
     static constexpr int kGroups = C::BK / 8;                 // KN: groups of 8 k rows a slab
+    static_assert(!KN || kGroups % C::NW == 0, "a load of all waves stays in one block of columns");
     const char *base;
     int64_t ld;          // bytes
     int rows, len;       // elements
     uint32_t off;        // this lane's offset in load 0
-    int chunk;           // REG: byte of the row (k or columns) this lane's chunk starts at
-    u32x4 reg[C::DMA ? 1 : kLoads];
+    u32x4 reg[C::DMA ? 1 : C::kSets][C::DMA ? 1 : kLoads];
 
+    static __device__ __forceinline__ int swizzle(int r) {
+        return !KN ? (r >> 1) & 7 : esz == 4 ? 0 : esz == 2 ? 4 * ((r >> 1) & 1) : r & 7;
+    }
     __device__ __forceinline__ void init(int wave, int lane) {
         const int r = 8 * wave + (lane >> 3);
-        const int swz = !KN ? (r >> 1) & 7 : esz == 2 ? 4 * ((r >> 1) & 1) : r & 7;
-        chunk = 16 * ((lane & 7) ^ swz);
-        off = (uint32_t)(r * (int)ld + chunk);
+        off = (uint32_t)(r * (int)ld + 16 * ((lane & 7) ^ swizzle(r)));
     }
     // First row (KN: k row) and first byte along the row of load j, over all waves.
     static __device__ __forceinline__ constexpr int row_of(int j) {
@@ -110,53 +116,57 @@ struct Loader {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
                                                  off + (uint32_t)(row_of(j) * (int)ld + byte_of(j)), 0, 0, 0);
     }
-    // REG: slab t into the staging registers.
-    __device__ __forceinline__ void hold(int t, int wave, int lane) {
+    // REG: slab t into staging set `set`, at offsets that the panel's last 16 bytes bound.  Where
+    // a row (or, KN, a row of the last columns) ends inside a chunk, what follows it in memory
+    // comes too; the panel's last chunk comes too early.  Both are put right by cut, in the last slab.
+    __device__ __forceinline__ void hold(int t, int set) {
         if constexpr (!C::DMA) {
-            const int64_t k0 = (int64_t)t * C::BK;
-            const int r0 = 8 * wave + (lane >> 3);
+            const int step = (int)ld, wide = (KN ? rows : len) * esz;
+            const int k0 = t * (KN ? C::BK : kSlab);                        // rows, or bytes of a row
+            const int first = KN ? min(k0, len - 1) : 0;
+            const int limit = (KN ? len - 1 - first : rows - 1) * step + wide - 16;
+            // From 16 bytes before: the last tile's columns may be fewer than a chunk.
+            const char *src = base + (int64_t)first * ld - 16;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int64_t r = row_of(j) + r0;
-                const int64_t b = byte_of(j) + chunk;
-                const int64_t row = KN ? k0 + r : r, last = KN ? len - 1 : rows - 1;
-                const int64_t byte = KN ? b : b + k0 * esz, wide = (int64_t)(KN ? rows : len) * esz;
-                const int64_t from = byte < wide - 16 ? byte : wide - 16;
-                const char *src = base + (row < last ? row : last) * ld + from;
-                u32x4 v = reinterpret_cast<const Bytes16 *>(src)->v;
-                if ((KN ? byte_of(j) : k0 * esz) + kSlab > wide) {          // a slab that holds the row's end
-                    const int64_t shift = byte - from;
-                    const u128 w = shift < 16 ? __builtin_bit_cast(u128, v) >> (8 * (int)shift) : (u128)0;
-                    v = __builtin_bit_cast(u32x4, w);
-                }
-                if (KN && row > last) v = u32x4{};
-                reg[j] = v;
+                const int at = min((int)off + row_of(j) * step + (KN ? byte_of(j) : k0), limit);
+                reg[set][j] = reinterpret_cast<const Bytes16 *>(src + (uint32_t)(at + 16))->v;
             }
         }
     }
-    __device__ __forceinline__ void stash(char *stage, int wave, int lane) const {
+    __device__ __forceinline__ void stash(char *stage, int set, int wave, int lane) const {
         if constexpr (!C::DMA) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                *reinterpret_cast<u32x4 *>(stage + (j * C::NW + wave) * 1024 + lane * 16) = reg[j];
+                *reinterpret_cast<u32x4 *>(stage + (j * C::NW + wave) * 1024 + lane * 16) = reg[set][j];
         }
     }
-    // Zero the bytes from `from` on in every row of a slab: those past K, where the loads
-    // have brought what follows a row in memory.
-    __device__ __forceinline__ void cut(char *stage, int from) const {
-        if constexpr (!KN) {
-            for (int i = threadIdx.x; i < ROWS * 8; i += 64 * C::NW) {
-                const int r = i >> 3, c = i & 7;
-                u32x4 *at = reinterpret_cast<u32x4 *>(stage + r * kSlab + 16 * (c ^ ((r >> 1) & 7)));
-                if (16 * c + 16 <= from) continue;
-                u32x4 v = *at;
+    // Slab t, the last one, in LDS: zero what lies past K, and (REG) move the panel's last chunk
+    // to its place.
+    __device__ __forceinline__ void cut(int t, char *stage) const {
+        if (KN && C::DMA) return;                                // k rows past the last were read as zero
+        const int left = KN ? len - t * C::BK : len * esz - t * kSlab;
+        const int wide = KN ? rows * esz : left;
+        for (int i = threadIdx.x; i < ROWS * 8; i += 64 * C::NW) {
+            const int r = KN ? (i >> 3) % C::BK : i >> 3;
+            const int byte = 16 * ((i & 7) ^ swizzle(r)) + (KN ? kSlab * ((i >> 3) / C::BK) : 0);
+            const int past = byte + 16 - wide;                   // bytes of the chunk past the row's end
+            const bool moved = !C::DMA && r == (KN ? left : rows) - 1 && past > 0 && past < 16;
+            if (!moved && (KN ? r < left : past <= 0)) continue;
+            u32x4 *at = reinterpret_cast<u32x4 *>(stage + 16 * i);
+            u32x4 v = *at;
+            if (moved)
+                v = __builtin_bit_cast(u32x4, __builtin_bit_cast(u128, v) >> (8 * past));
+            if (KN) {
+                if (r >= left) v = u32x4{};
+            } else {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const int n = from - 16 * c - 4 * d;            // valid bytes from here on
+                    const int n = 16 - past - 4 * d;             // valid bytes from here on
                     v[d] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
                 }
-                *at = v;
             }
+            *at = v;
         }
     }
 };
@@ -182,6 +192,8 @@ template <class C, bool KN> __device__ __forceinline__ uint32_t frag_base(int f,
         const int row = 8 * (q >> 1) + (j16 >> 2);
         const int c = 2 * (q & 1) + ((j16 & 3) >> 1) + 4 * ((f & 1) ^ ((row >> 1) & 1));
         return (uint32_t)((f >> 1) * (C::BK * kSlab) + row * kSlab + 16 * c + 8 * (j16 & 1));
+    } else if constexpr (C::esz == 4) {
+        return (uint32_t)((32 * f + 4 * h) * kSlab + 4 * l32);
     } else {
         const int s16 = lane & 15;
         const int e = ((s16 >> 1) & 3) + 4 * (s16 >> 3);
@@ -198,7 +210,7 @@ __device__ __forceinline__ FragOf<C::esz> read_frag(const char *panel, uint32_t 
     if constexpr (!KN) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            // fp8: 32 consecutive bytes of each half; bf16: 16 bytes of each 32.
+            // fp8: 32 consecutive bytes of each half; bf16 and fp32: 16 bytes of each 32.
             const uint32_t flip = 16u * (C::esz == 1 ? 4 * (q >> 1) + (q & 1) : 2 * q);
             const u32x4 w = *reinterpret_cast<const u32x4 *>(panel + ((base ^ flip) + 32 * kSlab * i));
             if constexpr (C::esz == 1) {
@@ -216,6 +228,12 @@ __device__ __forceinline__ FragOf<C::esz> read_frag(const char *panel, uint32_t 
             const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 16 * kSlab * q + 4 * kSlab));
             v.q[q] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
+    } else if constexpr (C::esz == 4) {
+        const uint32_t *at = reinterpret_cast<const uint32_t *>(panel + (base + 32 * kSlab * i));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v.q[q][e] = at[(8 * q + e) * (kSlab / 4)];
     } else {
         const char *at = panel + (base ^ (32u * i));
 #pragma unroll
@@ -239,6 +257,22 @@ __device__ __forceinline__ f32x16 product_bf16(const FragOf<2> &a, const FragOf<
         acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b.q[i]),
                                                       __builtin_bit_cast(bf16x8, a.q[i]), acc, 0, 0, 0);
     return acc;
+}
+
+// The two lane halves' k of one instruction lie four apart (their 16 bytes), in both operands.
+__device__ __forceinline__ f32x16 product_f32(const FragOf<4> &a, const FragOf<4> &b, int half, f32x16 acc) {
+#pragma unroll
+    for (int i = 2 * half; i < 2 * half + 2; ++i) {
+        const f32x4 av = __builtin_bit_cast(f32x4, a.q[i]), bv = __builtin_bit_cast(f32x4, b.q[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bv[e], av[e], acc, 0, 0, 0);
+    }
+    return acc;
+}
+template <int ESZ> __device__ __forceinline__ f32x16 product(const FragOf<ESZ> &a, const FragOf<ESZ> &b, int half, f32x16 acc) {
+    if constexpr (ESZ == 1) return product_fp8(a, b, half, acc);
+    else if constexpr (ESZ == 2) return product_bf16(a, b, half, acc);
+    else return product_f32(a, b, half, acc);
 }
 
 template <class C>
@@ -299,10 +333,11 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     a.init(wave, lane);
     b.init(wave, lane);
 
-    // Slabs that are read as they land; where K ends inside a slab, that one is cut first.
+    // Slabs that are read as they land; the last one is put in order first where K ends inside it
+    // (always, if it came through registers).
     const int len = a.len;
-    const bool cut = C::DMA && (!C::AKN || !C::BKN) && len % C::BK != 0;
-    const int nk = cut ? len / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
+    const bool cut = !C::DMA || ((!C::AKN || !C::BKN) && len % C::BK != 0);
+    const int nk = cut ? (len - 1) / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
 
     const int l32 = lane & 31;
     // Scales of the block that slab t is go to LDS as the slab does, into its
@@ -361,18 +396,19 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             else a.load(ra, st, wave, l - NB);
         }
     };
-    auto fetch = [&](int t, char *st) __attribute__((always_inline)) {
+    auto fetch = [&](int t, char *st, int set) __attribute__((always_inline)) {
         if constexpr (C::DMA) {
             load(a.source(t), b.source(t), st, 0, NA + NB);
         } else {
-            a.hold(t, wave, lane);
-            b.hold(t, wave, lane);
+            a.hold(t, set);
+            b.hold(t, set);
         }
     };
-    auto stash = [&](char *st) {
-        a.stash(st, wave, lane);
-        b.stash(st + C::kA, wave, lane);
+    auto stash = [&](char *st, int set) __attribute__((always_inline)) {
+        a.stash(st, set, wave, lane);
+        b.stash(st + C::kA, set, wave, lane);
     };
+    constexpr int kSets = C::kSets;
 
     // fp8: the partial tile of one product is added while the next one is
     // multiplied, half of it behind each matrix instruction, so that a wave
@@ -395,7 +431,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     // Products of slab t, whose fragments (B's, and A's first) are in
     // registers, from stage `cur`; meanwhile slab t + 1 lands in `next`, whose
     // first fragments are read at the end, and slab t + 2 is sent for.
-    // `first`: the set that holds A's first fragment; `scales`: the slab's.
+    // `first`: the set that holds A's first fragment; `scales`: the slab's; `turn`: t modulo the
+    // loop's turn.
     //
     // With four steps a slab (kSpread) the loads go out one between two matrix
     // instructions, half of them behind the barrier and the rest in the next
@@ -406,7 +443,7 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     constexpr bool kSpread = C::DMA && NW == 8;
     constexpr int kFirst = NS == 2 ? (NA + NB) / 2 : NA + NB, kRest = NA + NB - kFirst;
     constexpr int kSlabLoads = NA + NB + (FP8 ? 1 : 0);
-    auto slab = [&](int t, char *cur, char *next, int first, float *scales) __attribute__((always_inline)) {
+    auto slab = [&](int t, char *cur, char *next, int first, float *scales, int turn) __attribute__((always_inline)) {
         // Addresses are made again from these in every slab: kept across the loop they would
         // take more registers than there are.
         asm volatile("" : "+v"(a_base), "+v"(b_base), "+v"(a.off), "+v"(b.off));
@@ -422,17 +459,21 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             if (i + 1 < FM) {
                 fa[s ^ 1] = read_a(cur, i + 1);
             } else {
-                stash(next);
-                // Slab t + 1 has landed; of three stages, slab t + 2's loads may be under way.
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * kSlabLoads));
+                stash(next, (turn + 1) % kSets);
+                // Slab t + 1 (and its scales) has landed; of three stages, or two sets of staging
+                // registers, slab t + 2's loads may be under way.
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(C::DMA ? (NS - 2) * kSlabLoads : (kSets - 1) * (NA + NB)));
                 __builtin_amdgcn_s_barrier();
                 fa[s ^ 1] = read_a(next, 0);
                 load_scales(t + NS, scales);
+                __builtin_amdgcn_sched_barrier(0);        // the waits count what was sent after the scales
                 if constexpr (kSpread) {
                     ra = a.source(t + NS);
                     rb = b.source(t + NS);
+                } else if constexpr (C::DMA) {
+                    fetch(t + NS, cur, 0);
                 } else {
-                    fetch(t + NS, cur);
+                    fetch(t + 1 + kSets, cur, (turn + 1) % kSets);     // the set that was put away
                 }
             }
             // The loads that go out in gap g (0 .. 2 * FN - 1) of this step.
@@ -444,14 +485,14 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const int n = i * FN + j;
-                if constexpr (FP8) part[n & 1] = product_fp8(fa[s], fb[j], 0, f32x16{});
-                else acc[i][j] = product_bf16(fa[s], fb[j], 0, acc[i][j]);
+                if constexpr (FP8) part[n & 1] = product<C::esz>(fa[s], fb[j], 0, f32x16{});
+                else acc[i][j] = product<C::esz>(fa[s], fb[j], 0, acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
                 if (kCarry || n > 0) add(n - 1, 0);
                 send(2 * j);
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (FP8) part[n & 1] = product_fp8(fa[s], fb[j], 1, part[n & 1]);
-                else acc[i][j] = product_bf16(fa[s], fb[j], 1, acc[i][j]);
+                if constexpr (FP8) part[n & 1] = product<C::esz>(fa[s], fb[j], 1, part[n & 1]);
+                else acc[i][j] = product<C::esz>(fa[s], fb[j], 1, acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
                 if (i + 1 == FM) fb[j] = read_b(next, j);
                 if (kCarry || n > 0) add(n - 1, 1);
@@ -467,15 +508,20 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     };
 
     if (len > 0) {
+        // In this order: the waits count on it.
         load_scales(0, scale0);
-        fetch(0, st0);
-        stash(st0);
+        fetch(0, st0, 0);
+        stash(st0, 0);
 #pragma unroll
         for (int i = 1; i < NS; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
             load_scales(i, scale_set(i));
+            __builtin_amdgcn_sched_barrier(0);
             if (kSpread) load(a.source(i), b.source(i), stage(i), 0, kFirst);
-            else fetch(i, stage(i));
+            else fetch(i, stage(i), i % kSets);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (!C::DMA && kSets > 1) fetch(2, st0, 0);
         // Slab 0 has landed when only the others' loads are left.
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 1) * ((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0))));
         __builtin_amdgcn_s_barrier();
@@ -488,27 +534,26 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         for (; t + kTurn <= nk; t += kTurn) {
 #pragma unroll
             for (int u = 0; u < kTurn; ++u)
-                slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u));
+                slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u), u);
         }
 #pragma unroll
         for (int u = 0; u < kTurn - 1; ++u)
-            if (t + u < nk) slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u));
+            if (t + u < nk) slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u), u);
         if (cut) {
             // Slab nk ends K.  It has landed (slab 0: the wait above), every
             // wave has read what it will of it, and it is read again.
             const int at = nk % NS;
             char *cur = stage(at), *next = stage((at + 1) % NS);
-            const int tail = (int)(((int64_t)len - (int64_t)nk * C::BK) * C::esz);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
             __builtin_amdgcn_s_barrier();
-            a.cut(cur, tail);
-            b.cut(cur + C::kA, tail);
+            a.cut(nk, cur);
+            b.cut(nk, cur + C::kA);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
             __builtin_amdgcn_s_barrier();
             fa[0] = read_a(cur, 0);
 #pragma unroll
             for (int j = 0; j < FN; ++j) fb[j] = read_b(cur, j);
-            slab(nk, cur, next, 0, scale_set(at));
+            slab(nk, cur, next, 0, scale_set(at), 0);
         }
         if (kCarry) {
             add(-1, 0);
@@ -625,9 +670,10 @@ constexpr TileCost kTileCosts[] = {
 // 600 and 520 us; 16 groups of 8192 x 4096 x 4096: 225, 235 and 195 us; 64
 // rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128).  Groups are taken to be
 // alike, with half an empty tile each at their ends.
-// `first`: the largest to consider.
+// `first`: the largest to consider; `matrix`: us of matrix instructions that
+// a slab of 128 x 128 takes, where they take longer than its loads (fp32).
 inline TileSize tile_size(double rows, double cols, double slabs, double groups, TileSize first,
-                          double tile_factor = 1.0) {
+                          double tile_factor = 1.0, double matrix = 0.0) {
     TileSize best = kTile32;
     double least = 0.0;
     for (int i = first; i <= kTile32; ++i) {
@@ -635,7 +681,9 @@ inline TileSize tile_size(double rows, double cols, double slabs, double groups,
         const double each = rows / groups / c.bm + 0.5;
         const double tiles = (groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm)) * std::ceil(cols / c.bn);
         const double turns = std::ceil(tiles / kComputeUnits);
-        const double t = std::max(turns * (slabs * c.slab + c.tile * tile_factor), slabs * c.alone + 6.0);
+        const double least_slab = matrix * c.bm * c.bn / (128 * 128);
+        const double t = std::max(turns * (slabs * std::max(c.slab, least_slab) + c.tile * tile_factor),
+                                  slabs * std::max(c.alone, least_slab) + 6.0);
         if (i == first || t < least) {
             least = t;
             best = static_cast<TileSize>(i);
@@ -644,18 +692,22 @@ inline TileSize tile_size(double rows, double cols, double slabs, double groups,
     return best;
 }
 
+constexpr double kMatrixF32 = 1.75;       // 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, 4 matrix cores
+
 template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParams &p, hipStream_t s) {
-    const double slabs = std::ceil((double)p.K * (DT == GEMM_DTYPE_FP8F32 ? 1 : 2) / kSlab);
+    constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32, F32 = DT == GEMM_DTYPE_F32;
+    const double slabs = std::ceil((double)p.K * (FP8 ? 1 : F32 ? 4 : 2) / kSlab);
     const double groups = p.ends != nullptr ? std::max(1, std::min(p.groups, p.M)) : 1;
-    // Staging registers leave room for fewer accumulators, partial tiles for fewer still.
-    constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32;
-    switch (tile_size(p.M, p.N, slabs, groups, DMA ? kTile256 : FP8 ? kTile64 : kTile128)) {
+    // Staging registers leave room for fewer accumulators, partial tiles for fewer still; fp32 is
+    // bound by the matrix cores at 128 x 128 already.
+    constexpr TileSize first = DMA && !F32 ? kTile256 : !DMA && FP8 ? kTile64 : kTile128;
+    switch (tile_size(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0)) {
         case kTile256:
-            if constexpr (DMA) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
+            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTileWide:
-            if constexpr (DMA) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
+            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
         case kTile128:
-            if constexpr (DMA || !FP8) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
+            if constexpr (first != kTile64) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
         case kTile64: return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
         default: return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA>>(p, s);
     }
@@ -663,6 +715,28 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
 template <int DT> hipError_t launch_typed(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t s) {
     if (op_b == GEMM_OP_N) return dma ? launch_sized<DT, true, true>(p, s) : launch_sized<DT, true, false>(p, s);
     return dma ? launch_sized<DT, false, true>(p, s) : launch_sized<DT, false, false>(p, s);
+}
+
+
+// Weight gradients: both operands are walked down their rows.  Results are
+// fp32, so a tile's store takes twice the time.
+template <int DT> hipError_t launch_wgrad(bool dma, const GroupedParams &p, hipStream_t s) {
+    constexpr bool F32 = DT == GEMM_DTYPE_F32;
+    // The outputs of all groups together, each as deep as a group has rows.
+    const double slabs = std::ceil((double)p.M / p.groups / (F32 ? 32 : 64));
+    switch (tile_size((double)p.N * p.groups, p.K, slabs, p.groups, dma && !F32 ? kTile256 : kTile128, 2.0,
+                      F32 ? kMatrixF32 : 0.0)) {
+        case kTile256:
+        case kTileWide:
+            if constexpr (!F32)
+                if (dma) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s);
+        case kTile128:
+            return dma ? launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, true>>(p, s)
+                       : launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, false>>(p, s);
+        default:
+            return dma ? launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, true>>(p, s)
+                       : launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, false>>(p, s);
+    }
 }
 
 }  // namespace
