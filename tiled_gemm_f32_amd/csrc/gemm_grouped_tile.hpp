@@ -56,9 +56,9 @@ typedef unsigned __int128 u128;
 
 constexpr int kSlab = 128;              // bytes of k a slab holds of every row
 
-// 16 bytes at any alignment of their elements.
-struct __attribute__((packed, aligned(1))) Bytes16 {
-    u32x4 v;
+// A vector at any alignment of its elements, which the hardware's global accesses take.
+template <class V> struct __attribute__((packed, aligned(1))) Anywhere {
+    V v;
 };
 
 template <int DT_, int FM_, int FN_, int WM_, int WN_, bool AKN_, bool BKN_, bool DMA_, int NS_ = 2>
@@ -130,7 +130,7 @@ struct Loader {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int at = min((int)off + row_of(j) * step + (KN ? byte_of(j) : k0), limit);
-                reg[set][j] = reinterpret_cast<const Bytes16 *>(src + (uint32_t)(at + 16))->v;
+                reg[set][j] = reinterpret_cast<const Anywhere<u32x4> *>(src + (uint32_t)(at + 16))->v;
             }
         }
     }
@@ -571,8 +571,6 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     float *of = static_cast<float *>(p.out) + out_at;
     uint16_t *oh = static_cast<uint16_t *>(p.out) + out_at;
     const bool bf16_out = !WGRAD && p.out_type == GEMM_OUT_BF16;
-    const uintptr_t at = bf16_out ? reinterpret_cast<uintptr_t>(oh) & 7 : reinterpret_cast<uintptr_t>(of) & 15;
-    const bool vec = at == 0 && p.ldo % 4 == 0;
     // The lane again, opaque: what is made of it stays out of the loop's registers.
     int elane = threadIdx.x & 63;
     asm volatile("" : "+v"(elane));
@@ -602,8 +600,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
             if (bf16_out) {
                 const uint32_t h0 = to_bf16(v[0]), h1 = to_bf16(v[1]), h2 = to_bf16(v[2]), h3 = to_bf16(v[3]);
-                if (vec && whole) {
-                    *reinterpret_cast<u32x2 *>(oh + o) = u32x2{h0 | (h1 << 16), h2 | (h3 << 16)};
+                if (whole) {
+                    reinterpret_cast<Anywhere<u32x2> *>(oh + o)->v = u32x2{h0 | (h1 << 16), h2 | (h3 << 16)};
                 } else {
                     const uint32_t hs[4] = {h0, h1, h2, h3};
 #pragma unroll
@@ -616,8 +614,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
                     for (int e = 0; e < 4; ++e)
                         if (col + e < out_cols) v[e] = fmaf(p.beta, of[o + e], v[e]);
                 }
-                if (vec && whole) {
-                    *reinterpret_cast<f32x4 *>(of + o) = v;
+                if (whole) {
+                    reinterpret_cast<Anywhere<f32x4> *>(of + o)->v = v;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
