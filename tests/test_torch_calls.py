@@ -1,0 +1,104 @@
+"""The torch wrappers' two ways: _torch_calls for the common case, Python for
+the rest.  Both give the same results, and _torch_calls answers None (so that
+the wrapper takes the call) to whatever it does not take."""
+import pytest
+import torch
+
+import tiled_gemm_f32_amd as tg
+
+F32, BF16, FP8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def calls():
+    tg.load()
+    from tiled_gemm_f32_amd import _torch_calls
+    return _torch_calls
+
+
+def test_calls_outside_the_common_case_are_left_to_the_wrappers(calls):
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    q, s = torch.zeros(4, 8, dtype=FP8), torch.ones(4, 1)
+    ends = torch.tensor([4], dtype=torch.int32)
+    for got in (calls.quantize(x, 1, 0, 0), calls.quantize(x, 7, 0, 0), calls.quantize(x, "1", 0, 0),
+                calls.quantize(None, 1, 0, 0), calls.quantize(x, 1), calls.quantize(x, 1, "0", 0),
+                calls.rms_norm(x, w, None, 1e-5, None, 0, 0), calls.rms_norm(x, None, x, 1e-5, FP8, 0, 0),
+                calls.rms_norm(x, w, None, "1e-5", 3, 0, 0), calls.rms_norm_backward(x, x, w, None, 1e-5, 0, 0),
+                calls.rms_norm_backward(x, x, w, 1, None, 0, 0), calls.block_gemm(q, q, s, s, "T", 1.0, None, 0, 0),
+                calls.block_gemm(q, q, None, None, "X", None, None, 0, 0),
+                calls.grouped_gemm(x, x[None], ends, None, None, "T", 1.0, None, 0, 0),
+                calls.grouped_gemm(1, 2, 3, 4, 5, 6, 7, 8, 0, 0), calls.grouped_wgrad(x, x, ends, 1.0, 0, 0),
+                calls.grouped_wgrad(x, x, None, None, 0, 0)):
+        assert got is None
+
+
+def same(a, b):
+    for p, q in zip(a if isinstance(a, tuple) else (a,), b if isinstance(b, tuple) else (b,)):
+        assert (p is None) == (q is None)
+        if p is not None:
+            assert p.dtype == q.dtype and p.shape == q.shape and p.stride() == q.stride() and p.device == q.device
+            assert torch.equal(p.contiguous().view(torch.uint8), q.contiguous().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 40, 24), (5, 1, 130), (33, 257, 1), (48, 256, 384)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_both_ways_give_the_same(gpu_available, calls, M, N, K, dtype):
+    print(f"[calls] {M}x{N}x{K} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(M + N + K)
+    here = torch.cuda.current_stream().cuda_stream        # a stream passed in: the wrapper's own way
+    x = torch.randn(M, K + 3, generator=g).to(dtype).cuda()[:, 1:K + 1]
+    w = torch.nn.Parameter(torch.randn(K, generator=g).to(dtype).cuda())
+    for rows in (1, 128):
+        same(tg.quantize(x, rows), tg.quantize(x, rows, stream=here))
+    for residual in (None, x + 1):
+        for kind in (None, F32, BF16, FP8):
+            same(tg.rms_norm(x, w, residual=residual, out_dtype=kind),
+                 tg.rms_norm(x, w, residual=residual, out_dtype=kind, stream=here))
+        same(tg.rms_norm_backward(x, x, w, dsum=residual), tg.rms_norm_backward(x, x, w, dsum=residual, stream=here))
+    qa, sa = tg.quantize(x)
+    ends = torch.tensor([M // 2, M // 2, M], dtype=torch.int32).cuda()
+    for op in "TN":
+        b = torch.randn(3, *((N, K) if op == "T" else (K, N)), generator=g).to(dtype).cuda()
+        codes, scales = zip(*(tg.quantize(m, 128) for m in b))
+        qb, sb = torch.stack([c.view(torch.uint8) for c in codes]).view(FP8), torch.stack(scales)
+        for kind in (None, F32):
+            same(tg.block_gemm(qa, qb[1], sa, sb[1], op_b=op, out_dtype=kind),
+                 tg.block_gemm(qa, qb[1], sa, sb[1], op_b=op, out_dtype=kind, stream=here))
+            same(tg.grouped_gemm(x, b, ends, op_b=op, alpha=0.5, out_dtype=kind),
+                 tg.grouped_gemm(x, b, ends, op_b=op, alpha=0.5, out_dtype=kind, stream=here))
+            same(tg.grouped_gemm(qa, qb, ends, a_scales=sa, b_scales=sb, op_b=op, out_dtype=kind),
+                 tg.grouped_gemm(qa, qb, ends, a_scales=sa, b_scales=sb, op_b=op, out_dtype=kind, stream=here))
+    dy = torch.randn(M, N, generator=g).to(dtype).cuda()
+    same(tg.grouped_wgrad(dy, x, ends), tg.grouped_wgrad(dy, x, ends, stream=here))
+
+
+@pytest.mark.gpu
+def test_refusals_are_the_wrappers(gpu_available, calls):
+    x = torch.zeros(4, 8, device="cuda")
+    w = torch.ones(8, device="cuda")
+    with pytest.raises(TypeError):
+        tg.quantize(x.half())
+    with pytest.raises(ValueError):
+        tg.quantize(x.t())
+    with pytest.raises(ValueError):
+        tg.rms_norm(x, w[:7])
+    with pytest.raises(TypeError):
+        tg.rms_norm(x, w.bfloat16())
+    with pytest.raises(ValueError):
+        tg.rms_norm(x, w, residual=x[:3])
+    with pytest.raises(TypeError):
+        tg.rms_norm(x, w, out_dtype=torch.float16)
+    with pytest.raises(tg.GemmError):
+        tg.rms_norm(x, w, eps=-1.0)
+    q, s = tg.quantize(x)
+    with pytest.raises(ValueError):
+        tg.block_gemm(q, q, s, None)
+    with pytest.raises(ValueError):
+        tg.block_gemm(q, q, s[:3], s[:1])
+    with pytest.raises(ValueError):
+        tg.grouped_gemm(x, x[None], torch.tensor([4, 4], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        tg.grouped_wgrad(x, x[:3], torch.tensor([4], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        tg.grouped_wgrad(x, x, torch.tensor([4], dtype=torch.int32, device="cuda"), beta=1.0)

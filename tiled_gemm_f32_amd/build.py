@@ -31,6 +31,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libgemm.so")
+CALLS_PATH = os.path.join(HERE, "_torch_calls.so")
 
 SOURCES = ["gemm_api.cpp", "gemm_f32_tiled.hip", "gemm_bf16_tiled.hip", "gemm_f32_skinny.hip", "gemm_fp8_tiled.hip",
            "gemm_general.hip", "gemm_bf16_skinny.hip", "gemm_skinny_nt.hip", "gemm_scratch.hip",
@@ -178,6 +179,26 @@ def resource_markdown(table: dict) -> str:
     return "\n".join(out) + "\n"
 
 
+def build_torch_calls() -> None:
+    """Compile _torch_calls.so, the torch wrappers' common calls (host code only).  The torch
+    libraries it names are those of the process that imports it, which has loaded torch first."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = CALLS_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-L", HERE, "-l:libgemm.so", "-Wl,-rpath,$ORIGIN"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{proc.stderr}")
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compile all kernels and the ABI; returns the path of libgemm.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -192,6 +213,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     if proc.returncode != 0:
         raise RuntimeError(f"link failed:\n{proc.stderr}")
     os.replace(tmp, LIB_PATH)
+    build_torch_calls()
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH

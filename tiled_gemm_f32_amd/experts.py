@@ -20,9 +20,42 @@ from ._lib import (
     gemm_quantize, gemm_rms_norm, gemm_rms_norm_backward, gemm_rms_norm_workspace_size)
 
 
-# A call costs the host about as long as a small kernel runs, so the checks
-# below are written for the common case: one attribute of a tensor read once,
-# devices compared as numbers, messages made only when something is wrong.
+# A call costs the host about as long as a small kernel runs.  The common ones
+# (outputs allocated here, the current device and stream) therefore go through
+# _torch_calls, which checks, allocates and forwards them without Python in
+# between, and answers None to anything else: that is done below, where the
+# checks read each attribute of a tensor once, compare devices as numbers, and
+# make messages only when something is wrong.
+
+class _NoCalls:
+    """Stands in for _torch_calls where it has not been built."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_calls = _device_of_calls = _stream_of_calls = None
+
+
+def _common(name: str, *args):
+    """The call in _torch_calls on the current device and stream; None if it is not one for it."""
+    global _calls, _device_of_calls, _stream_of_calls
+    if _calls is None:
+        import torch
+        from ._lib import load
+        load()
+        _device_of_calls, _stream_of_calls = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        try:
+            from . import _torch_calls
+            _calls = _torch_calls
+        except ImportError:
+            _calls = _NoCalls()
+    device = _device_of_calls()
+    got = getattr(_calls, name)(*args, device, _stream_of_calls(device))
+    if type(got) is int:
+        raise GemmError(got, name)
+    return got
+
 
 def _float_type(t, what: str) -> int:
     import torch
@@ -115,6 +148,10 @@ def quantize(x, block_rows: int = 1, out=None, scales=None, stream=None):
     (weights).  ``x`` is about ``codes * scale`` of each block.  Codes
     allocated here have rows padded to 16 bytes."""
     import torch
+    if out is None and scales is None and stream is None and x.is_cuda:
+        got = _common("quantize", x, block_rows)
+        if got is not None:
+            return got
     dt = _float_type(x, "x")
     device = _device(x, "x")
     _check(x, "x", device)
@@ -150,6 +187,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
     (``out_dtype``, by default x's type); with float8_e4m3fn ``scales`` holds
     a scale for every 128 columns of a row, otherwise it is None."""
     import torch
+    if out is None and summed is None and scales is None and stream is None and x.is_cuda:
+        got = _common("rms_norm", x, weight, residual, eps, out_dtype)
+        if got is not None:
+            return got
     dt = _float_type(x, "x")
     device = _device(x, "x")
     _check(x, "x", device)
@@ -203,6 +244,10 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
     alike (it may be passed as dy or dsum); dweight is float32, or None if it
     is not wanted."""
     import torch
+    if dx is None and want_dweight and stream is None and dy.is_cuda:
+        got = _common("rms_norm_backward", dy, summed, weight, dsum, eps)
+        if got is not None:
+            return got
     dt = _float_type(dy, "dy")
     device = _device(dy, "dy")
     _check(dy, "dy", device)
@@ -285,6 +330,10 @@ def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, ou
     the gradient of its input ("N") alike.  ``out`` is bfloat16 by default,
     or float32."""
     import torch
+    if out is None and stream is None and A.is_cuda:
+        got = _common("block_gemm", A, B, a_scales, b_scales, op_b, alpha, out_dtype)
+        if got is not None:
+            return got
     if op_b not in ("N", "T"):
         raise ValueError("op_b is 'N' or 'T'")
     device = _device(A, "A")
@@ -320,6 +369,10 @@ def grouped_gemm(A, B, ends, a_scales=None, b_scales=None, op_b: str = "T", alph
     dimension of groups).  Rows past the last end become zero.  ``out`` is
     float32 or bfloat16: by default A's type, bfloat16 for fp8."""
     import torch
+    if out is None and stream is None and A.is_cuda:
+        got = _common("grouped_gemm", A, B, ends, a_scales, b_scales, op_b, alpha, out_dtype)
+        if got is not None:
+            return got
     if op_b not in ("N", "T"):
         raise ValueError("op_b is 'N' or 'T'")
     fp8 = A.dtype == torch.float8_e4m3fn
@@ -353,6 +406,10 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
     in ``grouped_gemm``; ``out`` is float32, groups x N x K (allocated when
     None; then beta must be 0).  A group without rows gives beta * out[g]."""
     import torch
+    if out is None and beta == 0.0 and stream is None and dy.is_cuda:
+        got = _common("grouped_wgrad", dy, x, ends, alpha)
+        if got is not None:
+            return got
     dt = _float_type(dy, "dy")
     device = _device(dy, "dy")
     _check(dy, "dy", device)
