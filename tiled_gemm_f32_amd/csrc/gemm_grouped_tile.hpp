@@ -646,9 +646,9 @@ template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStr
                            stream);
 }
 
-// Tiles and how long they take: 256 x 256 and 128 x 256 (eight waves, the
-// latter on three stages), 128 x 128, 64 x 128 and 32 x 128 (four waves).
-enum TileSize { kTile256, kTileWide, kTile128, kTile64, kTile32 };
+// Tiles and how long they take: 256 x 256, 192 x 256 and 128 x 256 (eight
+// waves, the last on three stages), 128 x 128, 64 x 128 and 32 x 128 (four waves).
+enum TileSize { kTile256, kTile192, kTileWide, kTile128, kTile64, kTile32 };
 
 struct TileCost {
     int bm, bn;
@@ -658,7 +658,7 @@ struct TileCost {
     double slab, tile, alone;
 };
 constexpr TileCost kTileCosts[] = {
-    {256, 256, 1.6, 8.0, 1.2}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.78}, {64, 128, 0.40, 2.5, 0.5},
+    {256, 256, 1.6, 8.0, 1.2}, {192, 256, 1.26, 7.5, 0.95}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.78}, {64, 128, 0.40, 2.5, 0.5},
     {32, 128, 0.33, 1.2, 0.45}};
 
 // The tile of the least time over `rows` rows of an output of `cols` columns,
@@ -666,7 +666,8 @@ constexpr TileCost kTileCosts[] = {
 // product (2048 x 4096 x 4096 fp8: 42 us in 128 x 256, 50 in 128 x 128, 57
 // in 256 x 256, which leaves half of the compute units idle; 8192^3: 560,
 // 600 and 520 us; 16 groups of 8192 x 4096 x 4096: 225, 235 and 195 us; 64
-// rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128).  Groups are taken to be
+// rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128; 8 groups of 8192
+// x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).  Groups are taken to be
 // alike, with half an empty tile each at their ends.
 // `first`: the largest to consider; `matrix`: us of matrix instructions that
 // a slab of 128 x 128 takes, where they take longer than its loads (fp32).
@@ -702,6 +703,8 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     switch (tile_size(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0)) {
         case kTile256:
             if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
+        case kTile192:
+            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTileWide:
             if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
         case kTile128:
@@ -725,6 +728,7 @@ template <int DT> hipError_t launch_wgrad(bool dma, const GroupedParams &p, hipS
     switch (tile_size((double)p.N * p.groups, p.K, slabs, p.groups, dma && !F32 ? kTile256 : kTile128, 2.0,
                       F32 ? kMatrixF32 : 0.0)) {
         case kTile256:
+        case kTile192:
         case kTileWide:
             if constexpr (!F32)
                 if (dma) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s);

@@ -351,10 +351,25 @@ rms_norm_backward_kernel(NormGradParams p) {
         }
     }
     if (p.dweight == nullptr) return;
+    if constexpr (TEAMS > 1) {
+        // One partial row a workgroup: its teams' sums are added through LDS, in order.
+        __shared__ __attribute__((aligned(16))) float sums[TEAMS][PER * THREADS * kChunk];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int col = kChunk * (t + i * THREADS);
-        store8<GEMM_DTYPE_F32>(p.partials, (int64_t)team * N + col, dw[i], N - col);
+        for (int i = 0; i < PER; ++i)
+            *reinterpret_cast<f32x8 *>(&sums[threadIdx.x / THREADS][kChunk * (t + i * THREADS)]) = dw[i];
+        __syncthreads();
+        for (int col = threadIdx.x; col < N; col += TEAMS * THREADS) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < TEAMS; ++i) v += sums[i][col];
+            p.partials[(int64_t)blockIdx.x * N + col] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int col = kChunk * (t + i * THREADS);
+            store8<GEMM_DTYPE_F32>(p.partials, (int64_t)team * N + col, dw[i], N - col);
+        }
     }
 }
 
@@ -526,7 +541,7 @@ template <int DT> hipError_t norm_type(const NormParams &p, hipStream_t s) {
 int grad_workgroups(int64_t M, int64_t N) {
     const Shape sh = shape_of(N);
     const int64_t rows = sh == kWave2 ? (M + 3) / 4 : M;     // rows a workgroup takes at once: 4, or 1
-    const int64_t most = sh == kWave2 ? 512 : sh == kFour2 ? 1024 : 512;
+    const int64_t most = sh == kFour2 ? 768 : 512;
     return (int)(rows < most ? rows : most);
 }
 
@@ -550,7 +565,7 @@ template <int DT> hipError_t grad_type(const NormGradParams &p, hipStream_t s) {
 
 int norm_grad_partials(int64_t M, int64_t N) {
     if (M <= 0 || N <= 0) return 0;
-    return grad_workgroups(M, N) * (shape_of(N) == kWave2 ? 4 : 1);
+    return grad_workgroups(M, N);
 }
 
 hipError_t launch_rms_norm(const NormParams &p, hipStream_t s) {
