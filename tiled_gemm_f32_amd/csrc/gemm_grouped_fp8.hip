@@ -2,6 +2,12 @@
 #include "gemm_grouped_tile.hpp"
 
 namespace gemm {
+namespace {
+
+// The others are made as the launchers below name them.
+template __global__ void grouped_tile_kernel<TileConfig<GEMM_DTYPE_FP8F32, 4, 2, 2, 4, false, false, true>>(GroupedParams, int, int);
+
+}  // namespace
 
 hipError_t launch_grouped_fp8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream) {
     return launch_typed<GEMM_DTYPE_FP8F32>(op_b, dma, p, stream);
