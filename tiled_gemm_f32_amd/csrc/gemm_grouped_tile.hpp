@@ -281,11 +281,14 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     constexpr int FM = C::FM, FN = C::FN, NW = C::NW, BM = C::BM, BN = C::BN;
     constexpr bool FP8 = C::DT == GEMM_DTYPE_FP8F32, WGRAD = C::AKN;
     constexpr int NS = C::NS;
-    static_assert(NS == 2 || (NS == 3 && FM % 2 == 0 && C::DMA), "");
+    static_assert(NS == 2 || (NS <= 4 && C::DMA), "");
     // One array a stage: the compiler can then tell that a read of one does not depend on
     // loads still landing in another.
-    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage], st2[NS > 2 ? C::kStage : 16];
-    auto stage = [&](int i) __attribute__((always_inline)) -> char * { return i == 0 ? st0 : i == 1 ? st1 : st2; };
+    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
+    __shared__ __attribute__((aligned(1024))) char st2[NS > 2 ? C::kStage : 16], st3[NS > 3 ? C::kStage : 16];
+    auto stage = [&](int i) __attribute__((always_inline)) -> char * {
+        return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
+    };
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -347,9 +350,10 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     // tenth of the whole call.
     constexpr int kScaleA = (BM + 63) / 64;
     static_assert(!FP8 || kScaleA < NW, "a wave for each 64 rows and one for the columns");
-    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1], scale2[FP8 && NS > 2 ? NW * 64 : 1];
+    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1];
+    __shared__ float scale2[FP8 && NS > 2 ? NW * 64 : 1], scale3[FP8 && NS > 3 ? NW * 64 : 1];
     auto scale_set = [&](int i) __attribute__((always_inline)) -> float * {
-        return i == 0 ? scale0 : i == 1 ? scale1 : scale2;
+        return i == 0 ? scale0 : i == 1 ? scale1 : i == 2 ? scale2 : scale3;
     };
     const float *sc_base = nullptr;
     int64_t sc_step = 0;
@@ -460,8 +464,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
                 fa[s ^ 1] = read_a(cur, i + 1);
             } else {
                 stash(next, (turn + 1) % kSets);
-                // Slab t + 1 (and its scales) has landed; of three stages, or two sets of staging
-                // registers, slab t + 2's loads may be under way.
+                // Slab t + 1 (and its scales) has landed; of three stages or more, or two sets of
+                // staging registers, later slabs' loads may be under way.
                 __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(C::DMA ? (NS - 2) * kSlabLoads : (kSets - 1) * (NA + NB)));
                 __builtin_amdgcn_s_barrier();
                 fa[s ^ 1] = read_a(next, 0);
@@ -530,15 +534,15 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         for (int j = 0; j < FN; ++j) fb[j] = read_b(st0, j);
         int t = 0;
         // Whole turns of the stages as straight-line code, then the rest.
-        constexpr int kTurn = FM % 2 == 0 ? NS : 2;
+        constexpr int kTurn = FM * NS % 2 == 0 ? NS : 2 * NS;
         for (; t + kTurn <= nk; t += kTurn) {
 #pragma unroll
             for (int u = 0; u < kTurn; ++u)
-                slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u), u);
+                slab(t + u, stage(u % NS), stage((u + 1) % NS), (u * FM) & 1, scale_set(u % NS), u);
         }
 #pragma unroll
         for (int u = 0; u < kTurn - 1; ++u)
-            if (t + u < nk) slab(t + u, stage(u), stage((u + 1) % NS), (u * FM) & 1, scale_set(u), u);
+            if (t + u < nk) slab(t + u, stage(u % NS), stage((u + 1) % NS), (u * FM) & 1, scale_set(u % NS), u);
         if (cut) {
             // Slab nk ends K.  It has landed (slab 0: the wait above), every
             // wave has read what it will of it, and it is read again.
@@ -658,8 +662,18 @@ struct TileCost {
     double slab, tile, alone;
 };
 constexpr TileCost kTileCosts[] = {
-    {256, 256, 1.6, 8.0, 1.2}, {192, 256, 1.26, 7.5, 0.95}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.78}, {64, 128, 0.40, 2.5, 0.5},
-    {32, 128, 0.33, 1.2, 0.45}};
+    {256, 256, 1.6, 8.0, 1.2}, {192, 256, 1.26, 7.5, 0.95}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.6}, {64, 128, 0.40, 2.5, 0.38},
+    {32, 128, 0.33, 1.2, 0.25}};
+
+// `turn`: every compute unit gets one workgroup at most, and nothing hides
+// its loads but loads of its own: the small tiles then take four stages
+// (1024 x 2048 x 4096 bf16 in 64 x 128: 41 us on two stages, 27.5 on four; 64 x
+// 4096 x 4096 in 32 x 128: 36.6 and 18.2), which otherwise cost more in
+// workgroups a compute unit than they bring.
+struct TileChoice {
+    TileSize size;
+    bool turn;
+};
 
 // The tile of the least time over `rows` rows of an output of `cols` columns,
 // `slabs` slabs deep, in `groups` groups: large ones move the fewest bytes a
@@ -667,13 +681,13 @@ constexpr TileCost kTileCosts[] = {
 // in 256 x 256, which leaves half of the compute units idle; 8192^3: 560,
 // 600 and 520 us; 16 groups of 8192 x 4096 x 4096: 225, 235 and 195 us; 64
 // rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128; 8 groups of 8192
-// x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).  Groups are taken to be
-// alike, with half an empty tile each at their ends.
+// x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).
+// Groups are taken to be alike, with half an empty tile each at their ends.
 // `first`: the largest to consider; `matrix`: us of matrix instructions that
 // a slab of 128 x 128 takes, where they take longer than its loads (fp32).
-inline TileSize tile_size(double rows, double cols, double slabs, double groups, TileSize first,
-                          double tile_factor = 1.0, double matrix = 0.0) {
-    TileSize best = kTile32;
+inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first,
+                              double tile_factor = 1.0, double matrix = 0.0) {
+    TileChoice best = {};
     double least = 0.0;
     for (int i = first; i <= kTile32; ++i) {
         const TileCost &c = kTileCosts[i];
@@ -685,7 +699,7 @@ inline TileSize tile_size(double rows, double cols, double slabs, double groups,
                                   slabs * std::max(c.alone, least_slab) + 6.0);
         if (i == first || t < least) {
             least = t;
-            best = static_cast<TileSize>(i);
+            best = {static_cast<TileSize>(i), turns <= 1.0};
         }
     }
     return best;
@@ -700,7 +714,8 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     // Staging registers leave room for fewer accumulators, partial tiles for fewer still; fp32 is
     // bound by the matrix cores at 128 x 128 already.
     constexpr TileSize first = DMA && !F32 ? kTile256 : !DMA && FP8 ? kTile64 : kTile128;
-    switch (tile_size(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0)) {
+    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0);
+    switch (c.size) {
         case kTile256:
             if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTile192:
@@ -708,9 +723,18 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
         case kTileWide:
             if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
         case kTile128:
+            // (The others' products of a 128 x 128 slab cover its loads.)
+            if constexpr (DMA && DT == GEMM_DTYPE_BF16F32)
+                if (c.turn) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
             if constexpr (first != kTile64) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
-        case kTile64: return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
-        default: return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA>>(p, s);
+        case kTile64:
+            if constexpr (DMA)
+                if (c.turn) return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
+            return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
+        default:
+            if constexpr (DMA)
+                if (c.turn) return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA, 4>>(p, s);
+            return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA>>(p, s);
     }
 }
 template <int DT> hipError_t launch_typed(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t s) {
@@ -725,8 +749,8 @@ template <int DT> hipError_t launch_wgrad(bool dma, const GroupedParams &p, hipS
     constexpr bool F32 = DT == GEMM_DTYPE_F32;
     // The outputs of all groups together, each as deep as a group has rows.
     const double slabs = std::ceil((double)p.M / p.groups / (F32 ? 32 : 64));
-    switch (tile_size((double)p.N * p.groups, p.K, slabs, p.groups, dma && !F32 ? kTile256 : kTile128, 2.0,
-                      F32 ? kMatrixF32 : 0.0)) {
+    switch (tile_choice((double)p.N * p.groups, p.K, slabs, p.groups, dma && !F32 ? kTile256 : kTile128, 2.0,
+                        F32 ? kMatrixF32 : 0.0).size) {
         case kTile256:
         case kTile192:
         case kTileWide:
