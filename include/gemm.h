@@ -470,8 +470,9 @@ GEMM_API int32_t gemm_tuning_load(const char *path);
  * 2^-100)) in fp32.  Infinities and NaN become the NaN code and do not
  * count in amax.  Row i of Q starts at Q + i*ldq (ldq >= K); the scale of row
  * block i and column block j is scales[i*lds + j] (lds >= ceil(K / 128),
- * ceil(M / block_rows) rows).  The matrix-core paths of the products below
- * need rows of Q on 16 bytes: a multiple of 16 for ldq.
+ * ceil(M / block_rows) rows).  The products below read
+ * rows of Q that start on 16 bytes (ldq a multiple of 16) straight into LDS;
+ * other rows go through registers and run on smaller tiles.
  */
 GEMM_API gemm_status gemm_quantize(int32_t dtype, int32_t block_rows, int64_t M, int64_t K,
                                    const void *X, int64_t ldx, uint8_t *Q, int64_t ldq,

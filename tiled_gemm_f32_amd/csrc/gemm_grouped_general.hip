@@ -1,20 +1,19 @@
-// Grouped and block-scaled products for every operand type, layout, stride
-// and alignment, and the fp32 ones' only kernel.
+// Grouped and block-scaled products of the calls that the tiles do not take:
+// a row of an operand is shorter than one 16-byte load, rows lie so far apart
+// that a tile's panel passes the 2 GiB a buffer load can address, or the block
+// scales do.  Every type, layout, stride and alignment is right here.
 //
-// The blocked method: an output tile of 128 x 128 (or 64 x 64, where there
-// are too few large ones to fill the compute units), 32-deep slices of both
+// The blocked method: an output tile of 64 x 64, 32-deep slices of both
 // operands staged through registers into double-buffered LDS, four waves
 // each keeping a quarter of the tile in fp32 accumulators, products on
 // v_mfma_f32_32x32x2_f32 (exact products for all three types).  Operands are
-// read in units of 4 elements along the direction they are contiguous in,
-// one 16-byte load a unit where fp32 alignment allows, four element loads
-// otherwise, and widened to fp32 on the way to LDS; fp8 values take their
+// read element by element in units of 4 along the direction they are
+// contiguous in and widened to fp32 on the way to LDS; fp8 values take their
 // block scale there (one fp32 rounding, 2^-24, a value).  Both panels sit in
 // LDS as [row][k], so one consume loop serves every layout.
 //
-// fp32 is bound by the matrix cores (32 x 32 x 2 takes 64 cycles for 512 bytes
-// of fragments, a fifth of what LDS delivers); 128 x 128 tiles ask L2 for 16
-// bytes a cycle and compute unit.
+// Products this short are bound by their results' stores, and rows this far
+// apart by one memory transaction a row; larger tiles would change neither.
 #include "gemm_grouped.hpp"
 
 namespace gemm {
@@ -35,12 +34,13 @@ template <> struct Elem<GEMM_DTYPE_FP8F32> {
 };
 
 constexpr int kThreads = 256;
+constexpr int BT = 64;                 // rows and columns of a tile
 constexpr int kBK = 32;
 constexpr int kStride = kBK + 4;       // floats a panel row takes in LDS
 
 // One panel: `rows` of at most BT rows and `len` values of k at `base`.
 // KCONT: element (r, k) at base[r * ld + k]; otherwise at base[k * ld + r].
-template <int DT, int BT, bool KCONT, bool VEC>
+template <int DT, bool KCONT>
 struct Panel {
     typedef typename Elem<DT>::T T;
     static constexpr int kPer = BT * kBK / 4 / kThreads;     // units of 4 a thread
@@ -70,9 +70,7 @@ struct Panel {
             const bool in = KCONT ? r < rows : k < len;
             const T *src = base + (KCONT ? (int64_t)r * ld + k : (int64_t)k * ld + r);
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (VEC && in && left >= 4) {
-                v = *reinterpret_cast<const f32x4 *>(src);
-            } else if (in) {
+            if (in) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (e < left) v[e] = Elem<DT>::widen(src[e]);
@@ -103,16 +101,15 @@ struct Panel {
 
 // WGRAD: rows of the result are columns of dY (A), its columns those of X
 // (B), and k runs over the rows of one group.
-template <int DT, int BT, bool WGRAD, bool BN, bool VEC>
+template <int DT, bool WGRAD, bool BN>
 __global__ void __launch_bounds__(kThreads)
 grouped_general_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     typedef typename Elem<DT>::T T;
-    constexpr int F = BT / 64;            // 32 x 32 fragments a wave and direction
     __shared__ __attribute__((aligned(16))) float lds_a[2][BT * kStride];
     __shared__ __attribute__((aligned(16))) float lds_b[2][BT * kStride];
 
-    Panel<DT, BT, !WGRAD, VEC> a;
-    Panel<DT, BT, !WGRAD && !BN, VEC> b;
+    Panel<DT, !WGRAD> a;
+    Panel<DT, !WGRAD && !BN> b;
     int n0, group, row0;
     float *of = static_cast<float *>(p.out);
     uint16_t *oh = static_cast<uint16_t *>(p.out);
@@ -156,30 +153,16 @@ grouped_general_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const int h = lane >> 5, l32 = lane & 31;
-    f32x16 acc[F][F];
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
+    f32x16 acc = {};
     // Lane (l32, h) takes k = 16h .. 16h + 15 of its row; each matrix
     // instruction takes one k from each lane half.
     auto consume = [&](int buf) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            f32x4 fa[F], fb[F];
+            const f32x4 fa = *reinterpret_cast<const f32x4 *>(&lds_a[buf][(wm * 32 + l32) * kStride + 16 * h + 4 * q]);
+            const f32x4 fb = *reinterpret_cast<const f32x4 *>(&lds_b[buf][(wn * 32 + l32) * kStride + 16 * h + 4 * q]);
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                const int at = 32 * f + l32;
-                fa[f] = *reinterpret_cast<const f32x4 *>(&lds_a[buf][(wm * 32 * F + at) * kStride + 16 * h + 4 * q]);
-                fb[f] = *reinterpret_cast<const f32x4 *>(&lds_b[buf][(wn * 32 * F + at) * kStride + 16 * h + 4 * q]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < F; ++i)
-#pragma unroll
-                    for (int j = 0; j < F; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
+            for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[e], fb[e], acc, 0, 0, 0);
         }
     };
 
@@ -207,31 +190,26 @@ grouped_general_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     }
 
     // Register r of lane (h, l32) is row 8*(r/4) + 4*h + r%4, column l32 of its block.
+    const int col = wn * 32 + l32;
+    if (col >= b.rows) return;
 #pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int col = wn * 32 * F + 32 * j + l32;
-            if (col >= b.rows) continue;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = wm * 32 * F + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (row >= a.rows) continue;
-                const int64_t at = (int64_t)row * p.ldo + col;
-                float v = p.alpha * acc[i][j][r];
-                if (WGRAD) {
-                    if (p.beta != 0.0f) v = fmaf(p.beta, of[at], v);
-                    of[at] = v;
-                } else if (p.out_type == GEMM_OUT_BF16) {
-                    oh[at] = to_bf16(v);
-                } else {
-                    of[at] = v;
-                }
-            }
+    for (int r = 0; r < 16; ++r) {
+        const int row = wm * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (row >= a.rows) continue;
+        const int64_t at = (int64_t)row * p.ldo + col;
+        float v = p.alpha * acc[r];
+        if (WGRAD) {
+            if (p.beta != 0.0f) v = fmaf(p.beta, of[at], v);
+            of[at] = v;
+        } else if (p.out_type == GEMM_OUT_BF16) {
+            oh[at] = to_bf16(v);
+        } else {
+            of[at] = v;
         }
+    }
 }
 
-template <int DT, int BT, bool WGRAD, bool BN, bool VEC>
+template <int DT, bool WGRAD, bool BN>
 hipError_t launch(const GroupedParams &p, hipStream_t stream) {
     GroupedParams args = p;
     int tiles_m, tiles_n;
@@ -246,50 +224,25 @@ hipError_t launch(const GroupedParams &p, hipStream_t stream) {
         grid = dim3((unsigned)(tiles_m * tiles_n));
     }
     void *argv[] = {&args, &tiles_m, &tiles_n};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_general_kernel<DT, BT, WGRAD, BN, VEC>), grid,
+    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_general_kernel<DT, WGRAD, BN>), grid,
                            dim3(kThreads), argv, 0, stream);
 }
 
-bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// fp32 rows that start on 16 bytes take 16-byte loads.
-bool vectors(const GroupedParams &p) {
-    return on16(p.A) && on16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 && p.stride_b % 4 == 0;
-}
-
-template <int DT, int BT, bool WGRAD, bool BN>
-hipError_t launch_loads(const GroupedParams &p, hipStream_t s) {
-    if constexpr (DT == GEMM_DTYPE_F32)
-        if (vectors(p)) return launch<DT, BT, WGRAD, BN, true>(p, s);
-    return launch<DT, BT, WGRAD, BN, false>(p, s);
-}
-
-template <int DT, int BT, bool WGRAD>
-hipError_t launch_tile(int32_t op_b, const GroupedParams &p, hipStream_t s) {
-    if constexpr (WGRAD) return launch_loads<DT, BT, true, true>(p, s);
-    else return op_b == GEMM_OP_N ? launch_loads<DT, BT, false, true>(p, s) : launch_loads<DT, BT, false, false>(p, s);
-}
-
-// 128 x 128 where such tiles number at least the 256 compute units, else
-// 64 x 64, whose four times as many tiles keep them busy.
-template <int DT, bool WGRAD>
-hipError_t launch_type(int32_t op_b, const GroupedParams &p, hipStream_t s) {
-    const int64_t tiles = WGRAD ? (int64_t)((p.N + 127) / 128) * ((p.K + 127) / 128) * p.groups
-                                : most_row_tiles(p.M, p.groups, 128, p.ends != nullptr) * ((p.N + 127) / 128);
-    return tiles >= 256 ? launch_tile<DT, 128, WGRAD>(op_b, p, s) : launch_tile<DT, 64, WGRAD>(op_b, p, s);
+template <int DT> hipError_t launch_op(int32_t op_b, const GroupedParams &p, hipStream_t s) {
+    return op_b == GEMM_OP_N ? launch<DT, false, true>(p, s) : launch<DT, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream) {
-    if (dtype == GEMM_DTYPE_F32) return launch_type<GEMM_DTYPE_F32, false>(op_b, p, stream);
-    if (dtype == GEMM_DTYPE_BF16F32) return launch_type<GEMM_DTYPE_BF16F32, false>(op_b, p, stream);
-    return launch_type<GEMM_DTYPE_FP8F32, false>(op_b, p, stream);
+    if (dtype == GEMM_DTYPE_F32) return launch_op<GEMM_DTYPE_F32>(op_b, p, stream);
+    if (dtype == GEMM_DTYPE_BF16F32) return launch_op<GEMM_DTYPE_BF16F32>(op_b, p, stream);
+    return launch_op<GEMM_DTYPE_FP8F32>(op_b, p, stream);
 }
 
 hipError_t launch_wgrad_general(int32_t dtype, const GroupedParams &p, hipStream_t stream) {
-    if (dtype == GEMM_DTYPE_F32) return launch_type<GEMM_DTYPE_F32, true>(GEMM_OP_N, p, stream);
-    return launch_type<GEMM_DTYPE_BF16F32, true>(GEMM_OP_N, p, stream);
+    if (dtype == GEMM_DTYPE_F32) return launch<GEMM_DTYPE_F32, true, true>(p, stream);
+    return launch<GEMM_DTYPE_BF16F32, true, true>(p, stream);
 }
 
 }  // namespace gemm

@@ -2,13 +2,21 @@
 // gemm_grouped_f32.hip, gemm_grouped_bf16.hip and gemm_grouped_fp8.hip.
 //
 // A workgroup makes a tile of BM x BN outputs of one group, walking k in
-// slabs of 128 bytes a row (64 bf16 or 128 fp8 values: for fp8 exactly one
-// scale block).  Two LDS stages of a slab each: while a slab is multiplied
-// the next one lands in the other stage.  WM x WN waves each hold 32*FM x
-// 32*FN outputs; a wave keeps the slab's B fragments and two sets of A
-// fragments in registers, so every LDS byte of A is read once a wave and the
-// reads of A fragment i + 1 (or of the next slab) run under the products of
-// fragment i.
+// slabs of 128 bytes a row (32 fp32, 64 bf16 or 128 fp8 values: for fp8
+// exactly one scale block).  A ring of NS LDS stages holds a slab each: while
+// one is multiplied the next NS - 1 land in the others.  WM x WN waves each
+// hold 32*FM x 32*FN outputs; a wave keeps the slab's B fragments and two
+// sets of A fragments in registers, so every LDS byte of A is read once a
+// wave and the reads of A fragment i + 1 (or of the next slab) run under the
+// products of fragment i.
+//
+// Measured, and what bounds it: 8192^3 fp8 in 256 x 256 takes 470 to 500 us
+// (2.2 to 2.35 PF): a slab takes 1.6 us, of which its matrix instructions
+// alone would take 0.93 and its 64 KB 0.55 to 0.68 to land with every
+// compute unit loading.  8 groups of 8192 x 4096 x 2048 bf16: 138 us (1.0 PF;
+// a matrix product of 8192^3 reaches 1.1 to 1.5 here), bound by the power
+// limit on random data and by the last turn of tiles.  fp32 is bound by the matrix
+// cores (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads).
 //
 // fp8 with block scales: the matrix core sums a block of 128 k into a partial
 // tile of its own (two v_mfma_f32_32x32x64_f8f6f4, the first with a zero
@@ -728,9 +736,10 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
                 if (c.turn) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
             if constexpr (first != kTile64) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
         case kTile64:
-            if constexpr (DMA)
+            // (fp32 comes past here: twice 32 x 128 costs as much and starts sooner.)
+            if constexpr (DMA && !F32)
                 if (c.turn) return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
-            return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
+            if constexpr (!F32) return launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, false, BKN, DMA>>(p, s);
         default:
             if constexpr (DMA)
                 if (c.turn) return launch_grouped_tile<TileConfig<DT, 1, 1, 1, 4, false, BKN, DMA, 4>>(p, s);
