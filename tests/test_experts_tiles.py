@@ -72,6 +72,16 @@ def test_tiles_of_every_size(gpu_available, dtype, op, M, N, K):
     check_one(dtype, op, M, N, K)
 
 
+# Few tiles and a long k: its slabs shared out among a workgroup's waves, unevenly.
+@pytest.mark.parametrize("op", ["T", "N"])
+@pytest.mark.parametrize("dtype", [F32, BF16, FP8])
+@pytest.mark.parametrize("M,N,K", [(100, 520, 2111), (40, 2001, 4096), (250, 1000, 1043), (65, 129, 9000),
+                                   (70, 4000, 528), (1, 7000, 1500), (90, 90, 300)])
+def test_few_tiles_of_a_long_product(gpu_available, dtype, op, M, N, K):
+    say(f"[few tiles] {dtype} op={op} {M}x{N}x{K}")
+    check_one(dtype, op, M, N, K)
+
+
 def uneven(M, groups):
     """Rows of each group: the first of every four empty, the second a single row, the rest unlike each other."""
     part = [0 if g % 4 == 0 else 1 if g % 4 == 1 else 3 + 5 * g for g in range(groups)]

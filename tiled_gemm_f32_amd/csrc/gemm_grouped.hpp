@@ -150,6 +150,12 @@ hipError_t launch_grouped_f32(int32_t op_b, bool dma, const GroupedParams &p, hi
 // 16 bytes: the rows of the tile that suits, or 0 for calls that are not its.
 int skinny_rows(int32_t dtype, int32_t op_b, const GroupedParams &p);
 hipError_t launch_grouped_skinny(int32_t dtype, int rows, const GroupedParams &p, hipStream_t stream);
+// Few output tiles: whether the kernel whose waves share out k can run the call, and that kernel.
+constexpr int deep_columns(int32_t dtype, bool kn) {         // of its tiles of 32 rows
+    return !kn || dtype == GEMM_DTYPE_F32 ? 32 : dtype == GEMM_DTYPE_BF16F32 ? 64 : 128;
+}
+bool deep_takes(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p);
+hipError_t launch_grouped_deep(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_bf16(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_f32(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream);

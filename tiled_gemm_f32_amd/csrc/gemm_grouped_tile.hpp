@@ -73,13 +73,13 @@ template <int DT_, int FM_, int FN_, int WM_, int WN_, bool AKN_, bool BKN_, boo
 struct TileConfig {
     static constexpr int DT = DT_, FM = FM_, FN = FN_, WM = WM_, WN = WN_;
     static constexpr bool AKN = AKN_, BKN = BKN_, DMA = DMA_;
-    static constexpr int NS = NS_;                    // LDS stages
+    static constexpr int NS = DMA ? NS_ : 2;          // LDS stages
     static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
     static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : DT == GEMM_DTYPE_BF16F32 ? 2 : 4;
     static constexpr int BK = kSlab / esz;            // k a slab
-    // REG: slabs under way in registers.  Two where there is room: a small tile's products of one
-    // slab do not cover a load.
-    static constexpr int kSets = FM == 1 ? 2 : 1;
+    // REG: slabs under way in registers.  Two where there is room: a small tile's products
+    // of one slab do not cover a load.
+    static constexpr int kSets = DMA ? 1 : FM == 1 || (FM == 2 && !AKN) ? 2 : 1;
     static constexpr int kA = BM * kSlab, kB = BN * kSlab, kStage = kA + kB;
 };
 
@@ -95,6 +95,7 @@ struct Loader {
     int64_t ld;          // bytes
     int rows, len;       // elements
     uint32_t off;        // this lane's offset in load 0
+    uint32_t odd;        // NW == 1: in load 1, whose rows are swizzled as rows 8 .. 15 of 16
     u32x4 reg[C::DMA ? 1 : C::kSets][C::DMA ? 1 : kLoads];
 
     static __device__ __forceinline__ int swizzle(int r) {
@@ -103,7 +104,9 @@ struct Loader {
     __device__ __forceinline__ void init(int wave, int lane) {
         const int r = 8 * wave + (lane >> 3);
         off = (uint32_t)(r * (int)ld + 16 * ((lane & 7) ^ swizzle(r)));
+        odd = (uint32_t)(r * (int)ld + 16 * ((lane & 7) ^ swizzle(r + 8)));
     }
+    __device__ __forceinline__ uint32_t offset(int j) const { return !KN && C::NW == 1 && j % 2 == 1 ? odd : off; }
     // First row (KN: k row) and first byte along the row of load j, over all waves.
     static __device__ __forceinline__ constexpr int row_of(int j) {
         return KN ? 8 * ((j * C::NW) % kGroups) : 8 * C::NW * j;
@@ -122,7 +125,7 @@ struct Loader {
     }
     __device__ __forceinline__ void load(const rsrc_t &r, char *stage, int wave, int j) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
-                                                 off + (uint32_t)(row_of(j) * (int)ld + byte_of(j)), 0, 0, 0);
+                                                 offset(j) + (uint32_t)(row_of(j) * (int)ld + byte_of(j)), 0, 0, 0);
     }
     // REG: slab t into staging set `set`, at offsets that the panel's last 16 bytes bound.  Where
     // a row (or, KN, a row of the last columns) ends inside a chunk, what follows it in memory
@@ -137,7 +140,7 @@ struct Loader {
             const char *src = base + (int64_t)first * ld - 16;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int at = min((int)off + row_of(j) * step + (KN ? byte_of(j) : k0), limit);
+                const int at = min((int)offset(j) + row_of(j) * step + (KN ? byte_of(j) : k0), limit);
                 reg[set][j] = reinterpret_cast<const Anywhere<u32x4> *>(src + (uint32_t)(at + 16))->v;
             }
         }
@@ -150,12 +153,12 @@ struct Loader {
         }
     }
     // Slab t, the last one, in LDS: zero what lies past K, and (REG) move the panel's last chunk
-    // to its place.
-    __device__ __forceinline__ void cut(int t, char *stage) const {
+    // to its place.  tid: of the 64 * NW threads whose loads it was.
+    __device__ __forceinline__ void cut(int t, char *stage, int tid) const {
         if (KN && C::DMA) return;                                // k rows past the last were read as zero
         const int left = KN ? len - t * C::BK : len * esz - t * kSlab;
         const int wide = KN ? rows * esz : left;
-        for (int i = threadIdx.x; i < ROWS * 8; i += 64 * C::NW) {
+        for (int i = tid; i < ROWS * 8; i += 64 * C::NW) {
             const int r = KN ? (i >> 3) % C::BK : i >> 3;
             const int byte = 16 * ((i & 7) ^ swizzle(r)) + (KN ? kSlab * ((i >> 3) / C::BK) : 0);
             const int past = byte + 16 - wide;                   // bytes of the chunk past the row's end
@@ -523,19 +526,30 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         // In this order: the waits count on it.
         load_scales(0, scale0);
         fetch(0, st0, 0);
-        stash(st0, 0);
+        if constexpr (C::DMA) {
 #pragma unroll
-        for (int i = 1; i < NS; ++i) {
+            for (int i = 1; i < NS; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                load_scales(i, scale_set(i));
+                __builtin_amdgcn_sched_barrier(0);
+                if (kSpread) load(a.source(i), b.source(i), stage(i), 0, kFirst);
+                else fetch(i, stage(i), 0);
+            }
+        } else {
+            // Every set's loads go out before the first is waited for.
             __builtin_amdgcn_sched_barrier(0);
-            load_scales(i, scale_set(i));
+            load_scales(1, scale_set(1));
             __builtin_amdgcn_sched_barrier(0);
-            if (kSpread) load(a.source(i), b.source(i), stage(i), 0, kFirst);
-            else fetch(i, stage(i), i % kSets);
+#pragma unroll
+            for (int i = 1; i < kSets; ++i) fetch(i, st0, i);
+            __builtin_amdgcn_sched_barrier(0);
+            stash(st0, 0);
+            fetch(kSets, st0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (!C::DMA && kSets > 1) fetch(2, st0, 0);
         // Slab 0 has landed when only the others' loads are left.
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 1) * ((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0))));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(
+            C::DMA ? (NS - 1) * ((kSpread ? kFirst : NA + NB) + (FP8 ? 1 : 0)) : kSets * (NA + NB) + (FP8 ? 1 : 0)));
         __builtin_amdgcn_s_barrier();
         fa[0] = read_a(st0, 0);
 #pragma unroll
@@ -558,8 +572,8 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             char *cur = stage(at), *next = stage((at + 1) % NS);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
             __builtin_amdgcn_s_barrier();
-            a.cut(nk, cur);
-            b.cut(nk, cur + C::kA);
+            a.cut(nk, cur, threadIdx.x);
+            b.cut(nk, cur + C::kA, threadIdx.x);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
             __builtin_amdgcn_s_barrier();
             fa[0] = read_a(cur, 0);
@@ -571,7 +585,7 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
             add(-1, 0);
             add(-1, 1);
         }
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(C::DMA || FP8 ? 0 : 63));       // (what is under way to LDS)
         __builtin_amdgcn_s_barrier();
     }
 
@@ -681,6 +695,7 @@ constexpr TileCost kTileCosts[] = {
 struct TileChoice {
     TileSize size;
     bool turn;
+    double time;
 };
 
 // The tile of the least time over `rows` rows of an output of `cols` columns,
@@ -692,9 +707,10 @@ struct TileChoice {
 // x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).
 // Groups are taken to be alike, with half an empty tile each at their ends.
 // `first`: the largest to consider; `matrix`: us of matrix instructions that
-// a slab of 128 x 128 takes, where they take longer than its loads (fp32).
+// a slab of 128 x 128 takes, where they take longer than its loads (fp32);
+// `staged`: us that a lone workgroup's slab takes longer through registers.
 inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first,
-                              double tile_factor = 1.0, double matrix = 0.0) {
+                              double tile_factor = 1.0, double matrix = 0.0, double staged = 0.0) {
     TileChoice best = {};
     double least = 0.0;
     for (int i = first; i <= kTile32; ++i) {
@@ -704,13 +720,24 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
         const double turns = std::ceil(tiles / kComputeUnits);
         const double least_slab = matrix * c.bm * c.bn / (128 * 128);
         const double t = std::max(turns * (slabs * std::max(c.slab, least_slab) + c.tile * tile_factor),
-                                  slabs * std::max(c.alone, least_slab) + 6.0);
+                                  slabs * (std::max(c.alone, least_slab) + staged) + 6.0);
         if (i == first || t < least) {
             least = t;
-            best = {static_cast<TileSize>(i), turns <= 1.0};
+            best = {static_cast<TileSize>(i), turns <= 1.0, t};
         }
     }
     return best;
+}
+
+// Time of the kernel whose waves share out k (gemm_grouped_deep.hip) in tiles of 32 x bn: `each` us
+// for a wave's slab, eight slabs at a time, and one workgroup a compute unit.  Groups are unlike each
+// other, and a few tiles too many cost it a whole turn: a tenth is added to their number.  (16 x 4096
+// x 4096 fp8 against K x N weights: 12.1 us in 32 x 128, 9.3 so; 128 x 2000 x 8000 fp8: 21.8 and
+// 10.5; 64 x 1000 x 1024 fp32: 21.4 and 9.5; but 300 x 2000 x 4000 fp8, 630 tiles: 14.6 and 19.8.)
+inline double deep_time(double rows, double cols, double slabs, double groups, int bn, double each) {
+    const double high = rows / groups / 32 + 0.5;
+    const double tiles = (groups > 1 ? 1.1 * groups * std::max(1.0, high) : std::ceil(rows / 32)) * std::ceil(cols / bn);
+    return std::ceil(tiles / kComputeUnits) * (std::ceil(slabs / 8) * each + 4.0) + 2.5;
 }
 
 constexpr double kMatrixF32 = 1.75;       // 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, 4 matrix cores
@@ -720,16 +747,21 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     const double slabs = std::ceil((double)p.K * (FP8 ? 1 : F32 ? 4 : 2) / kSlab);
     const double groups = p.ends != nullptr ? std::max(1, std::min(p.groups, p.M)) : 1;
     // Staging registers leave room for fewer accumulators, partial tiles for fewer still; fp32 is
-    // bound by the matrix cores at 128 x 128 already.
-    constexpr TileSize first = DMA && !F32 ? kTile256 : !DMA && FP8 ? kTile64 : kTile128;
-    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0);
+    // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
+    // registers: 233 us in 128 x 128, 185 in 192 x 256.)
+    constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
+    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15);
+    constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
+    if (deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6) < c.time &&
+        deep_takes(DT, op, DMA, p))
+        return launch_grouped_deep(DT, op, DMA, p, s);
     switch (c.size) {
         case kTile256:
             if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTile192:
-            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
+            if constexpr (first <= kTile192) return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTileWide:
-            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, 3>>(p, s);
+            if constexpr (first <= kTileWide) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, DMA ? 3 : 2>>(p, s);
         case kTile128:
             // (The others' products of a 128 x 128 slab cover its loads.)
             if constexpr (DMA && DT == GEMM_DTYPE_BF16F32)
