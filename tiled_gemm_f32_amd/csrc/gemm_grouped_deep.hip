@@ -3,12 +3,19 @@
 //
 // A workgroup makes 32 rows by one 32-column fragment of one group, or by the
 // columns that 128 bytes of a k row hold where B is walked down k.  Its waves
-// take the slabs of 128 bytes of k in turn, each through LDS stages of its
-// own, so that the loop has no barrier and a compute unit has up to sixteen
-// slabs under way; the waves' partial tiles are added through LDS in a fixed
-// order.  A larger tile moves fewer bytes a product, but its slabs follow one
-// another: with no more tiles than compute units a call takes as long as one
-// tile's chain of slabs, which is an eighth here.
+// take the slabs of 128 bytes of k in turn, each through an LDS stage of its
+// own, so that the loop has no barrier; a slab's fragments are read into
+// registers at once, and the next one lands under their products.  The waves'
+// partial tiles are added through LDS in a fixed order.  A larger tile moves
+// fewer bytes a product, but its slabs follow one another: with no more tiles
+// than compute units a call takes as long as one tile's chain of slabs, which
+// is an eighth here.  (Two stages a wave, and so one workgroup a compute unit
+// instead of two, were no faster at 256 tiles and slower at more: 1000 x 512 x
+// 4096 bf16, 512 tiles, 17.4 us, 15.2 so.)
+//
+// 128 x 2000 x 8000 fp8 10.2 us (16 MB of weights: 1.6 TB/s, bound by the
+// latency of eight slabs a wave); 16 x 4096 x 4096 fp8 against K x N weights
+// 9.3 us; 64 x 1000 x 1024 fp32 9 us, 3.5 of them matrix instructions.
 //
 // Loads, layouts and fragments are those of gemm_grouped_tile.hpp with one
 // wave.  fp8: the products of the two block scales are made once a workgroup,
@@ -18,23 +25,21 @@
 namespace gemm {
 namespace {
 
-// Waves, stages a wave, and (fp8) floats of LDS beside the stages for 32 rows' scales: what fits
-// in 160 KB.  A single stage will do where a slab is large: its fragments are read into registers
-// at once, and the next slab lands under their products.
+// Waves, and (fp8) floats of LDS beside the stages for 32 rows' scales: two workgroups of
+// one-fragment tiles share a compute unit's 160 KB.
 template <class C> struct Deep {
-    static constexpr int kWaves = C::FN == 4 ? 7 : 8, kStages = C::FN == 1 ? 2 : 1;
-    static constexpr int kScales = C::DT != GEMM_DTYPE_FP8F32 ? 1 : C::FN == 4 ? 4864 : 7680;
+    static constexpr int kWaves = C::FN == 4 ? 7 : 8;
+    static constexpr int kScales = C::DT != GEMM_DTYPE_FP8F32 ? 1 : C::FN == 4 ? 4864 : 4000;
 };
-
 template <class C>
-__global__ void __launch_bounds__(64 * Deep<C>::kWaves, 2)
+__global__ void __launch_bounds__(64 * Deep<C>::kWaves, C::FN == 1 ? 4 : 2)
 grouped_deep_kernel(GroupedParams p, int tiles_n) {
     constexpr bool FP8 = C::DT == GEMM_DTYPE_FP8F32;
-    constexpr int FN = C::FN, BN = C::BN, WAVES = Deep<C>::kWaves, NS = Deep<C>::kStages;
+    constexpr int FN = C::FN, BN = C::BN, WAVES = Deep<C>::kWaves;
     constexpr int NA = Loader<C, false, 32>::kLoads, NB = Loader<C, C::BKN, BN>::kLoads;
-    static_assert(C::BM == 32 && C::NW == 1 && C::kSets >= (C::DMA ? 1 : NS), "");
+    static_assert(C::BM == 32 && C::NW == 1, "");
     static_assert(!C::BKN || BN * C::esz == kSlab, "a k row of the tile is a slab's 128 bytes");
-    __shared__ __attribute__((aligned(1024))) char st0[WAVES * C::kStage], st1[NS > 1 ? WAVES * C::kStage : 16];
+    __shared__ __attribute__((aligned(1024))) char stages[WAVES * C::kStage];
     __shared__ float scales[Deep<C>::kScales];
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
@@ -60,10 +65,8 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     a.init(0, lane);
     b.init(0, lane);
 
-    auto stage = [&](int u) __attribute__((always_inline)) -> char * {
-        return (u == 0 ? st0 : st1) + wave * C::kStage;
-    };
-    auto fetch = [&](int slab, char *st, int set) __attribute__((always_inline)) {
+    char *const st = stages + wave * C::kStage;
+    auto fetch = [&](int slab) __attribute__((always_inline)) {
         if constexpr (C::DMA) {
             const rsrc_t ra = a.source(slab), rb = b.source(slab);
 #pragma unroll
@@ -71,8 +74,8 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
 #pragma unroll
             for (int j = 0; j < NA; ++j) a.load(ra, st, 0, j);
         } else {
-            a.hold(slab, set);
-            b.hold(slab, set);
+            a.hold(slab, 0);
+            b.hold(slab, 0);
         }
     };
 
@@ -80,13 +83,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     f32x16 acc[FN] = {};
     // This wave's slabs: wave, wave + WAVES, ...
     const int mine = (slabs - wave + WAVES - 1) / WAVES;
-    if (mine > 0) {
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-            fetch(wave + u * WAVES, stage(u), u);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
+    if (mine > 0) fetch(wave);
     if constexpr (FP8) {
         const float *sa = p.sc.a + (int64_t)row0 * p.sc.a_row;
         const float *sb = p.sc.b + (int64_t)group * p.sc.b_group + (int64_t)(n0 / GEMM_SCALE_BLOCK) * p.sc.b_n;
@@ -97,16 +94,14 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
         __syncthreads();
     }
     const uint32_t a_base = frag_base<C, false>(0, lane), b_base = frag_base<C, C::BKN>(0, lane);
-    // Slab i of the wave's, from stage (and set) u = i % NS, which slab i + NS then goes to; `last`: it
-    // may end K.
-    auto step = [&](int i, int u, bool last) __attribute__((always_inline)) {
+    // Slab i of the wave's; `last`: it may end K.
+    auto step = [&](int i, bool last) __attribute__((always_inline)) {
         const int slab = wave + i * WAVES;
-        char *const st = stage(u);
         if constexpr (C::DMA) {
-            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 1) * (NA + NB)));
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
         } else {
-            a.stash(st, u, 0, lane);
-            b.stash(st + C::kA, u, 0, lane);
+            a.stash(st, 0, 0, lane);
+            b.stash(st + C::kA, 0, 0, lane);
         }
         if (last && (!C::DMA || len % C::BK != 0) && slab == slabs - 1) {
             a.cut(slab, st, lane);
@@ -117,9 +112,9 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[j] = read_frag<C, C::BKN>(st + C::kA, b_base, j);
         const float s = FP8 ? scales[32 * slab + l32] : 0.0f;
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));          // read before slab i + NS lands on them
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));          // read before the next slab lands on them
         __builtin_amdgcn_sched_barrier(0);
-        if (!last) fetch(slab + NS * WAVES, st, u);
+        if (!last) fetch(slab + WAVES);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -133,20 +128,11 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    int i = 0;
-    for (; i + NS < mine; i += NS) {
-#pragma unroll
-        for (int u = 0; u < NS; ++u) step(i + u, u, false);
-    }
-    // At most NS are left.  What was sent for past them is waited for too.
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-#pragma unroll
-    for (int u = 0; u < NS; ++u)
-        if (i + u < mine) step(i + u, u, true);
+    for (int i = 0; i + 1 < mine; ++i) step(i, false);
+    if (mine > 0) step(mine - 1, true);
 
     // Partial tiles: row l32 of 8 * FN chunks of 4 columns, chunk c at c ^ (row & 7).
-    float *const tile = reinterpret_cast<float *>(stage(0));
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    float *const tile = reinterpret_cast<float *>(st);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -157,7 +143,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     for (int e = tid; e < 32 * BN / 2; e += 64 * WAVES) {
         const int row = e / (BN / 2), col = 2 * (e % (BN / 2));
         if (row >= t.rows || col >= out_cols) continue;
-        const char *from = st0 + 4 * (BN * row + 4 * ((col >> 2) ^ (row & 7)) + (col & 3));
+        const char *from = stages + 4 * (BN * row + 4 * ((col >> 2) ^ (row & 7)) + (col & 3));
         float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
@@ -204,7 +190,7 @@ bool deep_takes(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p) {
     if (dtype == GEMM_DTYPE_FP8F32) {
         // (128 columns of a slab, their fragments and the partial tile leave no registers to stage through.)
         if (op_b == GEMM_OP_N && !dma) return false;
-        const int64_t most = op_b == GEMM_OP_N ? 4864 : 7680;       // Deep::kScales
+        const int64_t most = op_b == GEMM_OP_N ? 4864 : 4000;       // Deep::kScales
         if (((int64_t)p.K + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK * 32 > most) return false;
     }
     // (A launch counts its threads in 32 bits.)

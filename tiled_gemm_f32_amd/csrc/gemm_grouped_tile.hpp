@@ -708,7 +708,8 @@ struct TileChoice {
 // Groups are taken to be alike, with half an empty tile each at their ends.
 // `first`: the largest to consider; `matrix`: us of matrix instructions that
 // a slab of 128 x 128 takes, where they take longer than its loads (fp32);
-// `staged`: us that a lone workgroup's slab takes longer through registers.
+// `staged`: us that a lone workgroup's slab takes longer through registers, a
+// busy one's half as much.
 inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first,
                               double tile_factor = 1.0, double matrix = 0.0, double staged = 0.0) {
     TileChoice best = {};
@@ -719,7 +720,7 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
         const double tiles = (groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm)) * std::ceil(cols / c.bn);
         const double turns = std::ceil(tiles / kComputeUnits);
         const double least_slab = matrix * c.bm * c.bn / (128 * 128);
-        const double t = std::max(turns * (slabs * std::max(c.slab, least_slab) + c.tile * tile_factor),
+        const double t = std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
                                   slabs * (std::max(c.alone, least_slab) + staged) + 6.0);
         if (i == first || t < least) {
             least = t;
@@ -730,14 +731,15 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
 }
 
 // Time of the kernel whose waves share out k (gemm_grouped_deep.hip) in tiles of 32 x bn: `each` us
-// for a wave's slab, eight slabs at a time, and one workgroup a compute unit.  Groups are unlike each
-// other, and a few tiles too many cost it a whole turn: a tenth is added to their number.  (16 x 4096
+// for a wave's slab, eight slabs at a time.  Tiles of 32 columns share a compute unit by two, others
+// take it in turns; groups are unlike each other, so a tenth is added to the number of tiles.  (16 x 4096
 // x 4096 fp8 against K x N weights: 12.1 us in 32 x 128, 9.3 so; 128 x 2000 x 8000 fp8: 21.8 and
-// 10.5; 64 x 1000 x 1024 fp32: 21.4 and 9.5; but 300 x 2000 x 4000 fp8, 630 tiles: 14.6 and 19.8.)
+// 10.2; 64 x 1000 x 1024 fp32: 21.4 and 9; but 300 x 2000 x 4000 fp8, 630 tiles: 14.6 and 19.8.)
 inline double deep_time(double rows, double cols, double slabs, double groups, int bn, double each) {
     const double high = rows / groups / 32 + 0.5;
     const double tiles = (groups > 1 ? 1.1 * groups * std::max(1.0, high) : std::ceil(rows / 32)) * std::ceil(cols / bn);
-    return std::ceil(tiles / kComputeUnits) * (std::ceil(slabs / 8) * each + 4.0) + 2.5;
+    const double turns = tiles / kComputeUnits;
+    return (bn == 32 ? std::max(1.0, turns) : std::ceil(turns)) * (std::ceil(slabs / 8) * each + 4.0) + 2.5;
 }
 
 constexpr double kMatrixF32 = 1.75;       // 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, 4 matrix cores
