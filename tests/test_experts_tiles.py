@@ -152,7 +152,8 @@ def test_rows_far_apart(gpu_available, dtype, op, side):
 
 
 WGRADS = [(100, 8, 2000, 520), (100, 8, 2990, 520), (301, 3, 1500, 1111), (100, 8, 256, 1500), (100, 8, 130, 3001),
-          (2500, 8, 128, 1000), (100, 2, 128, 128), (1000, 8, 1500, 520), (77, 2, 1, 300), (77, 2, 300, 3)]
+          (2500, 8, 128, 1000), (4000, 3, 130, 264), (9000, 7, 65, 96), (50000, 64, 24, 40), (3200, 65, 40, 72),
+          (100, 2, 128, 128), (1000, 8, 1500, 520), (77, 2, 1, 300), (77, 2, 300, 3)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -167,6 +167,11 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
     p.alpha = alpha;
     p.beta = beta;
     const int64_t sz = (int64_t)esz;
+    // Deep groups are bound by their products, and the launch's end by the last of them (8 groups of
+    // 8192 x 4096 x 2048 bf16: 178 us in the order of their numbers, 165 so); shallow ones by the
+    // results' stores, which the larger groups' products hide if they come between (40 groups of
+    // 2000 x 1024 x 1024 bf16: 37 and 40).  Twelve slabs of 128 bytes a group's column.
+    p.by_size = groups <= 64 && M * sz >= 1536 * (int64_t)groups;
     const auto s = static_cast<hipStream_t>(stream);
     if (N * sz < 16 || K * sz < 16 || lddy * sz >= kMaxTileRow || ldx * sz >= kMaxTileRow)
         return launched(gemm::launch_wgrad_general(dtype, p, s));

@@ -26,6 +26,7 @@ struct GroupedParams {
     float alpha, beta;         // beta: weight gradients only
     int32_t out_type;          // GEMM_OUT_F32 or GEMM_OUT_BF16
     gemm_block_scales sc;      // fp8 only
+    bool by_size;              // weight gradients of at most 64 groups: in the order of their rows
 };
 
 // Most row tiles of `tile_m` rows that M rows in `groups` groups can make,
@@ -126,16 +127,30 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, i
     return t;
 }
 
-// Rows [lo, hi) of group g (weight gradients: one group a workgroup).
-__device__ __forceinline__ void find_group(const GroupedParams &p, int g, int &lo, int &hi) {
+// Rows [lo, hi) of the group that takes turn `turn` (weight gradients: one group a workgroup), and
+// that group.  by_size: those with the most rows go first, so that what is left for the launch's end
+// is short, a tile's time being its group's rows.
+__device__ __forceinline__ int find_group(const GroupedParams &p, int turn, int &lo, int &hi) {
     const int lane = threadIdx.x & 63;
-    int carry = 0;
-    for (int c = 0;; ++c) {
-        group_bounds(p, c, lane, carry, lo, hi);
-        if (g < 64 * (c + 1)) break;
+    int carry = 0, g = turn;
+    if (p.by_size) {
+        group_bounds(p, 0, lane, carry, lo, hi);
+        const int rows = lane < p.groups ? hi - lo : -1;
+        int before = 0;                                    // groups that go before this lane's
+        for (int i = 0; i < p.groups; ++i) {
+            const int other = __builtin_amdgcn_readlane(rows, i);
+            before += other > rows || (other == rows && i < lane);
+        }
+        g = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(before == turn)) - 1);
+    } else {
+        for (int c = 0;; ++c) {
+            group_bounds(p, c, lane, carry, lo, hi);
+            if (g < 64 * (c + 1)) break;
+        }
     }
     lo = __builtin_amdgcn_readfirstlane(__shfl(lo, g & 63));
     hi = __builtin_amdgcn_readfirstlane(__shfl(hi, g & 63));
+    return g;
 }
 
 #endif  // __HIPCC__

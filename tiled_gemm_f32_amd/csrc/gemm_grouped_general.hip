@@ -116,8 +116,7 @@ grouped_general_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     if (WGRAD) {
         int tm, tn, lo, hi;
         tile_coords(blockIdx.x, tiles_m, tiles_n, 8, tm, tn);
-        group = blockIdx.y;
-        find_group(p, group, lo, hi);
+        group = find_group(p, blockIdx.y, lo, hi);
         row0 = tm * BT;
         n0 = tn * BT;
         a.base = static_cast<const T *>(p.A) + (int64_t)lo * p.lda + row0;

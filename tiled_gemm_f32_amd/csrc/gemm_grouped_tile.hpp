@@ -313,8 +313,7 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     if (WGRAD) {
         int tm, tn, lo, hi;
         tile_coords(blockIdx.x, tiles_m, tiles_n, 4, tm, tn);
-        group = blockIdx.y;
-        find_group(p, group, lo, hi);
+        group = find_group(p, blockIdx.y, lo, hi);
         row0 = __builtin_amdgcn_readfirstlane(tm) * BM;
         n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
         a.base = A + ((int64_t)lo * p.lda + row0) * C::esz;
