@@ -41,10 +41,24 @@ inline int64_t most_row_tiles(int64_t M, int64_t groups, int64_t tile_m, bool gr
 #if defined(__HIPCC__)
 
 // A tile's rows: `rows` of them from row0; group is -1 for the rows past the
-// last end, which are zeroed; rows == 0: nothing to do.  tn: tile column.
+// last end, which are zeroed; rows <= 0: nothing to do.  tn: tile column.
+// parts: 1, or 2 or 4 where the tile is shared out, of which this is `part`.
 struct GroupTile {
-    int group, row0, rows, tn;
+    int group, row0, rows, tn, part, parts;
 };
+
+// Workgroups of tiles that come after the last whole turn of the compute
+// units: each tile goes to two of them, or to four, where all are then in one
+// turn.  wg becomes the tile's number.
+constexpr int kShareTurn = 256;
+__device__ __forceinline__ void share_out(int64_t tiles, int &wg, GroupTile &t) {
+    const int left = (int)(tiles % kShareTurn);
+    const int64_t past = wg - (tiles - left);
+    t.parts = left <= kShareTurn / 4 ? 4 : left <= kShareTurn / 2 ? 2 : 1;
+    if (past < 0) t.parts = 1;
+    t.part = past < 0 ? 0 : (int)past % t.parts;
+    if (past >= 0) wg = (int)(tiles - left + past / t.parts);
+}
 
 // Inclusive scans over the 64 lanes.
 __device__ __forceinline__ int wave_scan_max(int v, int lane) {
@@ -82,11 +96,20 @@ __device__ __forceinline__ void group_bounds(const GroupedParams &p, int chunk, 
 // The tile of workgroup `wg`, for tiles of tile_m rows and tiles_n columns of
 // tiles.  Tiles are walked in the order of tile_coords over the real number
 // of row tiles, so the dead workgroups of the launch are its last ones.
+template <bool SHARE = false>
 __device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, int tile_m, int tiles_n, int group_m) {
     GroupTile t;
+    t.part = 0;
+    t.parts = 1;
     if (p.ends == nullptr) {
         int tm;
-        tile_coords(wg, (p.M + tile_m - 1) / tile_m, tiles_n, group_m, tm, t.tn);
+        const int tiles_m = (p.M + tile_m - 1) / tile_m;
+        t.group = t.row0 = t.rows = t.tn = 0;
+        if (SHARE) {
+            share_out((int64_t)tiles_m * tiles_n, wg, t);
+            if (wg >= (int64_t)tiles_m * tiles_n) return t;
+        }
+        tile_coords(wg, tiles_m, tiles_n, group_m, tm, t.tn);
         t.group = 0;
         t.row0 = tm * tile_m;
         t.rows = min(tile_m, p.M - t.row0);
@@ -103,6 +126,7 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedParams &p, int wg, i
     }
     t.group = 0;
     t.row0 = t.rows = t.tn = 0;
+    if (SHARE) share_out((int64_t)total * tiles_n, wg, t);
     if ((int64_t)wg >= (int64_t)total * tiles_n) return t;
     int tm;
     tile_coords(wg, total, tiles_n, group_m, tm, t.tn);

@@ -5,7 +5,7 @@ namespace gemm {
 namespace {
 
 // The others are made as the launchers below name them.
-template __global__ void grouped_tile_kernel<TileConfig<GEMM_DTYPE_FP8F32, 4, 2, 2, 4, false, false, true>>(GroupedParams, int, int);
+template __global__ void grouped_tile_kernel<TileConfig<GEMM_DTYPE_FP8F32, 3, 2, 2, 4, false, false, true>>(GroupedParams, int, int);
 
 }  // namespace
 

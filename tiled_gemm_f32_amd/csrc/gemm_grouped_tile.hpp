@@ -286,17 +286,24 @@ template <int ESZ> __device__ __forceinline__ f32x16 product(const FragOf<ESZ> &
     else return product_f32(a, b, half, acc);
 }
 
+// Where a tile's operands and results are.
+struct Place {
+    const char *a, *b;
+    int64_t out;                  // elements
+    int rows, cols, len;          // of the tile, and its k
+    int group, row0, n0;
+};
+
+// A tile of one group, for all waves of a workgroup.  st, scale: LDS for NS stages and their scales, an
+// array each: the compiler can then tell that a read of one does not depend on loads still landing in
+// another.
 template <class C>
-__global__ void __launch_bounds__(64 * C::NW, 2)
-grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
+__device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &at, char *st0, char *st1, char *st2,
+                                          char *st3, float *scale0, float *scale1, float *scale2, float *scale3) {
     constexpr int FM = C::FM, FN = C::FN, NW = C::NW, BM = C::BM, BN = C::BN;
     constexpr bool FP8 = C::DT == GEMM_DTYPE_FP8F32, WGRAD = C::AKN;
     constexpr int NS = C::NS;
     static_assert(NS == 2 || (NS <= 4 && C::DMA), "");
-    // One array a stage: the compiler can then tell that a read of one does not depend on
-    // loads still landing in another.
-    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
-    __shared__ __attribute__((aligned(1024))) char st2[NS > 2 ? C::kStage : 16], st3[NS > 3 ? C::kStage : 16];
     auto stage = [&](int i) __attribute__((always_inline)) -> char * {
         return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
     };
@@ -304,43 +311,16 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
+    const int out_rows = at.rows, out_cols = at.cols, group = at.group, row0 = at.row0, n0 = at.n0;
+    const int64_t out_at = at.out;
 
     Loader<C, C::AKN, BM> a;
     Loader<C, C::BKN, BN> b;
-    int group, row0, n0, out_rows, out_cols;
-    int64_t out_at;
-    const char *A = static_cast<const char *>(p.A), *B = static_cast<const char *>(p.B);
-    if (WGRAD) {
-        int tm, tn, lo, hi;
-        tile_coords(blockIdx.x, tiles_m, tiles_n, 4, tm, tn);
-        group = find_group(p, blockIdx.y, lo, hi);
-        row0 = __builtin_amdgcn_readfirstlane(tm) * BM;
-        n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
-        a.base = A + ((int64_t)lo * p.lda + row0) * C::esz;
-        b.base = B + ((int64_t)lo * p.ldb + n0) * C::esz;
-        a.rows = out_rows = min(BM, p.N - row0);
-        b.rows = out_cols = min(BN, p.K - n0);
-        a.len = b.len = hi - lo;
-        out_at = (int64_t)group * p.stride_out + (int64_t)row0 * p.ldo + n0;
-    } else {
-        GroupTile t = find_tile(p, blockIdx.x, BM, tiles_n, 4);
-        // Integer divisions are vector code: make their results scalar again, so that the
-        // buffer resources below are.
-        t.group = __builtin_amdgcn_readfirstlane(t.group);
-        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-        t.tn = __builtin_amdgcn_readfirstlane(t.tn);
-        if (t.rows <= 0) return;
-        group = max(t.group, 0);
-        row0 = t.row0;
-        n0 = t.tn * BN;
-        a.base = A + (int64_t)row0 * p.lda * C::esz;
-        b.base = B + ((int64_t)group * p.stride_b + (C::BKN ? (int64_t)n0 : (int64_t)n0 * p.ldb)) * C::esz;
-        a.rows = out_rows = t.rows;
-        b.rows = out_cols = min(BN, p.N - n0);
-        a.len = b.len = t.group < 0 ? 0 : p.K;
-        out_at = (int64_t)row0 * p.ldo + n0;
-    }
+    a.base = at.a;
+    b.base = at.b;
+    a.rows = out_rows;
+    b.rows = out_cols;
+    a.len = b.len = at.len;
     a.ld = p.lda * C::esz;
     b.ld = p.ldb * C::esz;
     a.init(wave, lane);
@@ -360,8 +340,6 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     // tenth of the whole call.
     constexpr int kScaleA = (BM + 63) / 64;
     static_assert(!FP8 || kScaleA < NW, "a wave for each 64 rows and one for the columns");
-    __shared__ float scale0[FP8 ? NW * 64 : 1], scale1[FP8 ? NW * 64 : 1];
-    __shared__ float scale2[FP8 && NS > 2 ? NW * 64 : 1], scale3[FP8 && NS > 3 ? NW * 64 : 1];
     auto scale_set = [&](int i) __attribute__((always_inline)) -> float * {
         return i == 0 ? scale0 : i == 1 ? scale1 : i == 2 ? scale2 : scale3;
     };
@@ -555,14 +533,14 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         for (int j = 0; j < FN; ++j) fb[j] = read_b(st0, j);
         int t = 0;
         // Whole turns of the stages as straight-line code, then the rest.
-        constexpr int kTurn = FM * NS % 2 == 0 ? NS : 2 * NS;
-        for (; t + kTurn <= nk; t += kTurn) {
+        constexpr int kRound = FM * NS % 2 == 0 ? NS : 2 * NS;
+        for (; t + kRound <= nk; t += kRound) {
 #pragma unroll
-            for (int u = 0; u < kTurn; ++u)
+            for (int u = 0; u < kRound; ++u)
                 slab(t + u, stage(u % NS), stage((u + 1) % NS), (u * FM) & 1, scale_set(u % NS), u);
         }
 #pragma unroll
-        for (int u = 0; u < kTurn - 1; ++u)
+        for (int u = 0; u < kRound - 1; ++u)
             if (t + u < nk) slab(t + u, stage(u % NS), stage((u + 1) % NS), (u * FM) & 1, scale_set(u % NS), u);
         if (cut) {
             // Slab nk ends K.  It has landed (slab 0: the wait above), every
@@ -651,6 +629,84 @@ grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
     }
 }
 
+// The place of a tile that find_tile found, `shift` columns into its own.  Integer divisions are vector
+// code: their results are made scalar again, so that the buffer resources made of them are.
+template <class C>
+__device__ __forceinline__ Place place_of(const GroupedParams &p, const GroupTile &t, int tile_cols, int shift) {
+    Place at;
+    const int owner = __builtin_amdgcn_readfirstlane(t.group);
+    at.group = max(owner, 0);
+    at.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    at.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    at.n0 = __builtin_amdgcn_readfirstlane(t.tn) * tile_cols + shift;
+    at.cols = min(C::BN, p.N - at.n0);
+    at.len = owner < 0 ? 0 : p.K;
+    at.a = static_cast<const char *>(p.A) + (int64_t)at.row0 * p.lda * C::esz;
+    at.b = static_cast<const char *>(p.B) +
+           ((int64_t)at.group * p.stride_b + (C::BKN ? (int64_t)at.n0 : (int64_t)at.n0 * p.ldb)) * C::esz;
+    at.out = (int64_t)at.row0 * p.ldo + at.n0;
+    return at;
+}
+
+template <class C>
+__global__ void __launch_bounds__(64 * C::NW, 2)
+grouped_tile_kernel(GroupedParams p, int tiles_m, int tiles_n) {
+    constexpr int NS = C::NS, kScales = C::DT == GEMM_DTYPE_FP8F32 ? C::NW * 64 : 1;
+    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
+    __shared__ __attribute__((aligned(1024))) char st2[NS > 2 ? C::kStage : 16], st3[NS > 3 ? C::kStage : 16];
+    __shared__ float scale0[kScales], scale1[kScales], scale2[NS > 2 ? kScales : 1], scale3[NS > 3 ? kScales : 1];
+    Place at;
+    if constexpr (C::AKN) {
+        int tm, tn, lo, hi;
+        tile_coords(blockIdx.x, tiles_m, tiles_n, 4, tm, tn);
+        at.group = find_group(p, blockIdx.y, lo, hi);
+        at.row0 = __builtin_amdgcn_readfirstlane(tm) * C::BM;
+        at.n0 = __builtin_amdgcn_readfirstlane(tn) * C::BN;
+        at.rows = min(C::BM, p.N - at.row0);
+        at.cols = min(C::BN, p.K - at.n0);
+        at.len = hi - lo;
+        at.a = static_cast<const char *>(p.A) + ((int64_t)lo * p.lda + at.row0) * C::esz;
+        at.b = static_cast<const char *>(p.B) + ((int64_t)lo * p.ldb + at.n0) * C::esz;
+        at.out = (int64_t)at.group * p.stride_out + (int64_t)at.row0 * p.ldo + at.n0;
+    } else {
+        at = place_of<C>(p, find_tile(p, blockIdx.x, C::BM, tiles_n, 4), C::BN, 0);
+        if (at.rows <= 0) return;
+    }
+    make_tile<C>(p, at, st0, st1, st2, st3, scale0, scale1, scale2, scale3);
+}
+
+// The same, where the tiles past the last whole turn of the compute units are
+// shared out: 128 x 256 to each of two workgroups, or 128 x 128 to each of
+// four.  Tiles of at most 128 rows, groups' last ones, are made as 128 x 256.
+// (8 groups of 8192 x 2048 x 4096 bf16, 1.1 turns: 159 us in whole tiles of 192 x
+// 256, 151 so; 16 groups of 8192 x 4096 x 4096 fp8, 2.5 turns: 187 to 204 and 179
+// to 193.)
+template <class C, class HALF, class QUARTER>
+__global__ void __launch_bounds__(64 * C::NW, 2)
+grouped_shared_kernel(GroupedParams p, int tiles_n) {
+    constexpr int kScales = C::DT == GEMM_DTYPE_FP8F32 ? C::NW * 64 : 1;
+    static_assert(C::NS == 2 && HALF::NS == 2 && QUARTER::NS == 2 && C::BM == 256 && C::BN == 256, "");
+    __shared__ __attribute__((aligned(1024))) char st0[C::kStage], st1[C::kStage];
+    __shared__ float scale0[kScales], scale1[kScales];
+    GroupTile t = find_tile<true>(p, blockIdx.x, C::BM, tiles_n, 4);
+    t.parts = __builtin_amdgcn_readfirstlane(t.parts);
+    t.part = __builtin_amdgcn_readfirstlane(t.part);
+    if (t.parts > 1) {
+        const int below = (t.parts == 4 ? t.part >> 1 : t.part) * 128;
+        t.row0 += below;
+        t.rows = min(t.rows - below, 128);
+    }
+    if (t.parts == 4) {
+        const Place at = place_of<QUARTER>(p, t, C::BN, 128 * (t.part & 1));
+        if (at.rows > 0 && at.cols > 0) make_tile<QUARTER>(p, at, st0, st1, st1, st1, scale0, scale1, scale1, scale1);
+        return;
+    }
+    Place at = place_of<C>(p, t, C::BN, 0);
+    if (at.rows <= 0) return;
+    if (at.rows <= 128) make_tile<HALF>(p, at, st0, st1, st1, st1, scale0, scale1, scale1, scale1);
+    else make_tile<C>(p, at, st0, st1, st1, st1, scale0, scale1, scale1, scale1);
+}
+
 constexpr int kComputeUnits = 256;
 
 template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStream_t stream) {
@@ -669,6 +725,18 @@ template <class C> hipError_t launch_grouped_tile(const GroupedParams &p, hipStr
     void *argv[] = {&args, &tiles_m, &tiles_n};
     return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_tile_kernel<C>), grid, dim3(64 * C::NW), argv, 0,
                            stream);
+}
+
+template <int DT, bool BKN> hipError_t launch_grouped_shared(const GroupedParams &p, hipStream_t stream) {
+    typedef TileConfig<DT, 4, 2, 2, 4, false, BKN, true> C;
+    typedef TileConfig<DT, 2, 2, 2, 4, false, BKN, true> HALF;
+    typedef TileConfig<DT, 2, 1, 2, 4, false, BKN, true> QUARTER;
+    GroupedParams args = p;
+    int tiles_n = (p.N + C::BN - 1) / C::BN;
+    const int64_t tiles = most_row_tiles(p.M, p.groups, C::BM, p.ends != nullptr) * tiles_n;
+    void *argv[] = {&args, &tiles_n};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_shared_kernel<C, HALF, QUARTER>),
+                           dim3((unsigned)(tiles + kShareTurn)), dim3(64 * C::NW), argv, 0, stream);
 }
 
 // Tiles and how long they take: 256 x 256, 192 x 256 and 128 x 256 (eight
@@ -708,9 +776,11 @@ struct TileChoice {
 // `first`: the largest to consider; `matrix`: us of matrix instructions that
 // a slab of 128 x 128 takes, where they take longer than its loads (fp32);
 // `staged`: us that a lone workgroup's slab takes longer through registers, a
-// busy one's half as much.
+// busy one's half as much; `share`: 256 x 256 tiles past the last whole turn
+// go to two or four workgroups each.
 inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first,
-                              double tile_factor = 1.0, double matrix = 0.0, double staged = 0.0) {
+                              double tile_factor = 1.0, double matrix = 0.0, double staged = 0.0,
+                              bool share = false) {
     TileChoice best = {};
     double least = 0.0;
     for (int i = first; i <= kTile32; ++i) {
@@ -719,8 +789,16 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
         const double tiles = (groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm)) * std::ceil(cols / c.bn);
         const double turns = std::ceil(tiles / kComputeUnits);
         const double least_slab = matrix * c.bm * c.bn / (128 * 128);
-        const double t = std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
+        double t = std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
                                   slabs * (std::max(c.alone, least_slab) + staged) + 6.0);
+        if (share && i == kTile256) {
+            const double whole = std::floor(tiles / kComputeUnits), left = tiles - kComputeUnits * whole;
+            const double rest = left <= 0.0                  ? 0.0
+                                : left <= kComputeUnits / 4 ? slabs * 0.65 + 6.0
+                                : left <= kComputeUnits / 2 ? slabs * 1.15 + 7.0
+                                                            : slabs * c.slab + c.tile;
+            t = std::max(whole * (slabs * c.slab + c.tile) + rest, slabs * 0.65 + 6.0);
+        }
         if (i == first || t < least) {
             least = t;
             best = {static_cast<TileSize>(i), turns <= 1.0, t};
@@ -751,14 +829,14 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
     // registers: 233 us in 128 x 128, 185 in 192 x 256.)
     constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
-    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15);
+    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15, true);
     constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
     if (deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6) < c.time &&
         deep_takes(DT, op, DMA, p))
         return launch_grouped_deep(DT, op, DMA, p, s);
     switch (c.size) {
         case kTile256:
-            if constexpr (first == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, false, BKN, DMA>>(p, s);
+            if constexpr (first == kTile256) return launch_grouped_shared<DT, BKN>(p, s);
         case kTile192:
             if constexpr (first <= kTile192) return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTileWide:
