@@ -11,11 +11,14 @@
 // wave of eight, or two a wave of four.  Four waves leave room for two
 // workgroups a compute unit, whose starts and ends hide behind each other's
 // loads; eight cover the memory's latency where a call has no more workgroups
-// than compute units.  Workgroups
-// start at blocks spread over K and wrap around, so that rows a power of two
-// apart do not press on the same memory channels at once; where a column
-// starts depends on the column only, so a row's results do not depend on the
-// other rows and groups of a call.
+// than compute units.  Workgroups start at blocks spread over K and wrap
+// around, so that rows a power of two apart do not press on the same memory
+// channels at once; where a column starts depends on the column only, so a
+// row's results do not depend on the other rows and groups of a call.
+//
+// 16 x 8192 x 8192 fp8: 17.5 to 19 us (3.5 to 3.8 TB/s of weights; a third is
+// the launch and the first loads' latency).  64 rows over 32 experts of 4096 x
+// 4096 fp8, 26 of them with rows: 88 to 95 us (4.6 to 5 TB/s, a copy's rate).
 //
 // fp8 with block scales: a block is one scale block.  Its partial sums are
 // multiplied by a(row) * b(column block) as they are added; the products of

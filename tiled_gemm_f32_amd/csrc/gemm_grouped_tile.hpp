@@ -15,8 +15,8 @@
 // alone would take 0.93 and its 64 KB 0.55 to 0.68 to land with every
 // compute unit loading.  8 groups of 8192 x 4096 x 2048 bf16: 138 us (1.0 PF;
 // a matrix product of 8192^3 reaches 1.1 to 1.5 here), bound by the power
-// limit on random data and by the last turn of tiles.  fp32 is bound by the matrix
-// cores (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads).
+// limit on random data and by the last turn of tiles.  fp32 is bound by the
+// matrix cores (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads).
 //
 // fp8 with block scales: the matrix core sums a block of 128 k into a partial
 // tile of its own (two v_mfma_f32_32x32x64_f8f6f4, the first with a zero
@@ -280,7 +280,8 @@ __device__ __forceinline__ f32x16 product_f32(const FragOf<4> &a, const FragOf<4
     }
     return acc;
 }
-template <int ESZ> __device__ __forceinline__ f32x16 product(const FragOf<ESZ> &a, const FragOf<ESZ> &b, int half, f32x16 acc) {
+template <int ESZ>
+__device__ __forceinline__ f32x16 product(const FragOf<ESZ> &a, const FragOf<ESZ> &b, int half, f32x16 acc) {
     if constexpr (ESZ == 1) return product_fp8(a, b, half, acc);
     else if constexpr (ESZ == 2) return product_bf16(a, b, half, acc);
     else return product_f32(a, b, half, acc);
@@ -751,7 +752,8 @@ struct TileCost {
     double slab, tile, alone;
 };
 constexpr TileCost kTileCosts[] = {
-    {256, 256, 1.6, 8.0, 1.2}, {192, 256, 1.26, 7.5, 0.95}, {128, 256, 1.0, 7.0, 0.7}, {128, 128, 0.59, 4.5, 0.6}, {64, 128, 0.40, 2.5, 0.38},
+    {256, 256, 1.6, 8.0, 1.2},  {192, 256, 1.26, 7.5, 0.95}, {128, 256, 1.0, 7.0, 0.7},
+    {128, 128, 0.59, 4.5, 0.6}, {64, 128, 0.40, 2.5, 0.38},
     {32, 128, 0.33, 1.2, 0.25}};
 
 // `turn`: every compute unit gets one workgroup at most, and nothing hides
@@ -786,7 +788,8 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
     for (int i = first; i <= kTile32; ++i) {
         const TileCost &c = kTileCosts[i];
         const double each = rows / groups / c.bm + 0.5;
-        const double tiles = (groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm)) * std::ceil(cols / c.bn);
+        const double high = groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm);
+        const double tiles = high * std::ceil(cols / c.bn);
         const double turns = std::ceil(tiles / kComputeUnits);
         const double least_slab = matrix * c.bm * c.bn / (128 * 128);
         double t = std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
@@ -813,13 +816,14 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
 // x 4096 fp8 against K x N weights: 12.1 us in 32 x 128, 9.3 so; 128 x 2000 x 8000 fp8: 21.8 and
 // 10.2; 64 x 1000 x 1024 fp32: 21.4 and 9; but 300 x 2000 x 4000 fp8, 630 tiles: 14.6 and 19.8.)
 inline double deep_time(double rows, double cols, double slabs, double groups, int bn, double each) {
-    const double high = rows / groups / 32 + 0.5;
-    const double tiles = (groups > 1 ? 1.1 * groups * std::max(1.0, high) : std::ceil(rows / 32)) * std::ceil(cols / bn);
+    const double high = groups > 1 ? 1.1 * groups * std::max(1.0, rows / groups / 32 + 0.5) : std::ceil(rows / 32);
+    const double tiles = high * std::ceil(cols / bn);
     const double turns = tiles / kComputeUnits;
     return (bn == 32 ? std::max(1.0, turns) : std::ceil(turns)) * (std::ceil(slabs / 8) * each + 4.0) + 2.5;
 }
 
-constexpr double kMatrixF32 = 1.75;       // 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, 4 matrix cores
+// 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, on four matrix cores.
+constexpr double kMatrixF32 = 1.75;
 
 template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParams &p, hipStream_t s) {
     constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32, F32 = DT == GEMM_DTYPE_F32;
@@ -829,7 +833,8 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
     // registers: 233 us in 128 x 128, 185 in 192 x 256.)
     constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
-    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15, true);
+    const TileChoice c =
+        tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15, true);
     constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
     if (deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6) < c.time &&
         deep_takes(DT, op, DMA, p))
@@ -838,14 +843,17 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
         case kTile256:
             if constexpr (first == kTile256) return launch_grouped_shared<DT, BKN>(p, s);
         case kTile192:
-            if constexpr (first <= kTile192) return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
+            if constexpr (first <= kTile192)
+                return launch_grouped_tile<TileConfig<DT, 3, 2, 2, 4, false, BKN, DMA>>(p, s);
         case kTileWide:
-            if constexpr (first <= kTileWide) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, DMA ? 3 : 2>>(p, s);
+            if constexpr (first <= kTileWide)
+                return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, DMA ? 3 : 2>>(p, s);
         case kTile128:
             // (The others' products of a 128 x 128 slab cover its loads.)
             if constexpr (DMA && DT == GEMM_DTYPE_BF16F32)
                 if (c.turn) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
-            if constexpr (first != kTile64) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
+            if constexpr (first != kTile64)
+                return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
         case kTile64:
             // (fp32 comes past here: twice 32 x 128 costs as much and starts sooner.)
             if constexpr (DMA && !F32)
