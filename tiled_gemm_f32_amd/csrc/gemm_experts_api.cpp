@@ -71,8 +71,8 @@ gemm_status run(const Product &c, gemm_stream_t stream) {
         c.groups > kMaxGroups)
         return GEMM_ERR_UNSUPPORTED;
     if (c.M == 0 || c.N == 0) return GEMM_OK;
-    // The smallest tile the kernels below fall back to is 64 x 64 (and only
-    // when there are few), so this bounds every launch.
+    // Bounds every launch: tiles of 32 x 128, the most there are, are at most twice these and of 256
+    // threads.  (The kernels of smaller tiles take fewer, and leave the others.)
     if (gemm::most_row_tiles(c.M, c.groups, 64, c.grouped) * ceil_div(c.N, 64) > kMaxTiles)
         return GEMM_ERR_UNSUPPORTED;
     gemm_status st = gemm::check_device();
