@@ -82,6 +82,17 @@ def test_few_tiles_of_a_long_product(gpu_available, dtype, op, M, N, K):
     check_one(dtype, op, M, N, K)
 
 
+# 256 x 256 tiles: one whole turn of 256 compute units and 64 tiles more (four workgroups to each), 121
+# (two to each), 144 (left whole); and the same at sizes that leave rows and columns of the parts empty.
+@pytest.mark.parametrize("op", ["T", "N"])
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("M,N,K", [(5000, 4096, 300), (3300, 7400, 272), (6400, 4096, 300), (4900, 3968, 256),
+                                   (3201, 7300, 390)])
+def test_tiles_past_the_last_whole_turn(gpu_available, dtype, op, M, N, K):
+    say(f"[last turn] {dtype} op={op} {M}x{N}x{K}")
+    check_one(dtype, op, M, N, K, pads=(0,), kinds=(F32,))
+
+
 def uneven(M, groups):
     """Rows of each group: the first of every four empty, the second a single row, the rest unlike each other."""
     part = [0 if g % 4 == 0 else 1 if g % 4 == 1 else 3 + 5 * g for g in range(groups)]
@@ -89,7 +100,8 @@ def uneven(M, groups):
     return part
 
 
-GROUPS = [(1000, 2900, 520, 16), (3000, 2900, 520, 32), (2000, 2890, 521, 32), (4000, 2000, 520, 32), (500, 1500, 527, 16)]
+GROUPS = [(1000, 2900, 520, 16), (3000, 2900, 520, 32), (2000, 2890, 521, 32), (4000, 2000, 520, 32), (500, 1500, 527, 16),
+          (8192, 2048, 600, 8), (9000, 2496, 304, 70)]
 
 
 @pytest.mark.parametrize("op", ["T", "N"])
