@@ -38,6 +38,15 @@ inline int64_t most_row_tiles(int64_t M, int64_t groups, int64_t tile_m, bool gr
     return c + (M - c) / tile_m;
 }
 
+// Operands walked down k that come through registers: the last offset, from a slab's first row on,
+// that one of its 16-byte loads may start at.  left: rows from there to the panel's end (1 at least);
+// step, wide: bytes between rows and of one.  The panel's end bounds its last slab; every other slab is
+// bounded by the row after its own bk, which a load that starts inside it reaches at most, so that the
+// offset stays in 32 bits however deep the panel is.
+constexpr int slab_limit(int left, int bk, int step, int wide) {
+    return (left <= bk ? left - 1 : bk) * step + wide - 16;
+}
+
 #if defined(__HIPCC__)
 
 // A tile's rows: `rows` of them from row0; group is -1 for the rows past the

@@ -135,7 +135,7 @@ struct Loader {
             const int step = (int)ld, wide = (KN ? rows : len) * esz;
             const int k0 = t * (KN ? C::BK : kSlab);                        // rows, or bytes of a row
             const int first = KN ? min(k0, len - 1) : 0;
-            const int limit = (KN ? len - 1 - first : rows - 1) * step + wide - 16;
+            const int limit = KN ? slab_limit(len - first, C::BK, step, wide) : (rows - 1) * step + wide - 16;
             // From 16 bytes before: the last tile's columns may be fewer than a chunk.
             const char *src = base + (int64_t)first * ld - 16;
 #pragma unroll
