@@ -32,7 +32,8 @@ def host_program(tmp_path, names, main):
     for name in names:
         at = text.index(name)
         at = text.rindex("\n", 0, at) + 1
-        source += text[at:text.index("\n}\n", at) + 3]
+        line = text[at:text.index("\n", at) + 1]
+        source += line if line.endswith("}\n") else text[at:text.index("\n}\n", at) + 3]
     (tmp_path / "t.cpp").write_text(source + main)
     exe = str(tmp_path / "t")
     subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-o", exe, str(tmp_path / "t.cpp")], check=True)
@@ -73,6 +74,21 @@ def test_a_slabs_loads_are_bounded_within_its_panel(tmp_path):
             assert limit == end - 16                       # the last slab's only clamped load is its last one
         else:                                              # no load of valid columns is clamped in another
             assert (bk - 1) * step + (wide - 1) // 16 * 16 <= limit
+
+
+def test_slabs_of_a_depth_near_2_to_the_31(tmp_path):
+    """Their number, the first row of each (and of the few that are sent for past the last), and the rows left."""
+    exe = host_program(tmp_path, ["constexpr int slabs_of", "constexpr int slab_first", "constexpr int slab_left"],
+                       "int main(){int t,b,l;while(scanf(\"%d %d %d\",&t,&b,&l)==3)"
+                       "printf(\"%d %d %d\\n\",slabs_of(l,b),slab_first(t,b,l),slab_left(t,b,l));}\n")
+    asked = []
+    for bk in (32, 64, 128):
+        for depth in (1, bk - 1, bk, bk + 1, 5 * bk, 10 ** 6 + 3, 2 ** 31 - 129, 2 ** 31 - 32, 2 ** 31 - 31, 2 ** 31 - 1):
+            slabs = -(-depth // bk)
+            asked += [(t, bk, depth) for t in {0, slabs // 2, slabs - 1, *range(slabs, slabs + 6)}]
+    got = answers(exe, asked)
+    for i, (t, bk, depth) in enumerate(asked):
+        assert got[3 * i:3 * i + 3] == [-(-depth // bk), min(t * bk, depth - 1), depth - t * bk], (t, bk, depth)
 
 
 def wide_rows(rows, cols, ld, dtype, seed):

@@ -47,6 +47,14 @@ constexpr int slab_limit(int left, int bk, int step, int wide) {
     return (left <= bk ? left - 1 : bk) * step + wide - 16;
 }
 
+// Slabs of bk that len takes, the first row of slab t (of one past the end: the last row), and the rows
+// from slab t's first one on (zero or less past the end), of len up to 2^31 - 1 and a few slabs more.
+constexpr int slabs_of(int len, int bk) { return (int)(((int64_t)len + bk - 1) / bk); }
+constexpr int slab_first(int t, int bk, int len) {
+    return (int)((uint32_t)t * (uint32_t)bk < (uint32_t)len ? (uint32_t)t * (uint32_t)bk : (uint32_t)len - 1);
+}
+constexpr int slab_left(int t, int bk, int len) { return (int)((uint32_t)len - (uint32_t)t * (uint32_t)bk); }
+
 #if defined(__HIPCC__)
 
 // A tile's rows: `rows` of them from row0; group is -1 for the rows past the

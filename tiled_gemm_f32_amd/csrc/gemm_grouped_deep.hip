@@ -79,7 +79,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
         }
     };
 
-    const int slabs = (int)(((int64_t)len + C::BK - 1) / C::BK);
+    const int slabs = slabs_of(len, C::BK);
     f32x16 acc[FN] = {};
     // This wave's slabs: wave, wave + WAVES, ...
     const int mine = (slabs - wave + WAVES - 1) / WAVES;

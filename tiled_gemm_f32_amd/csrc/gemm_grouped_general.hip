@@ -65,10 +65,10 @@ struct Panel {
         for (int i = 0; i < kPer; ++i) {
             int r, k;
             coord(i, r, k);
-            k += k0;
-            const int left = KCONT ? len - k : rows - r;     // valid elements from here on
-            const bool in = KCONT ? r < rows : k < len;
-            const T *src = base + (KCONT ? (int64_t)r * ld + k : (int64_t)k * ld + r);
+            const int rest = len - k0 - k;                   // (k0 + k itself may pass 2^31)
+            const int left = KCONT ? rest : rows - r;        // valid elements from here on
+            const bool in = KCONT ? r < rows : rest > 0;
+            const T *src = base + (KCONT ? (int64_t)r * ld + k0 + k : ((int64_t)k0 + k) * ld + r);
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
             if (in) {
 #pragma unroll
@@ -76,7 +76,7 @@ struct Panel {
                     if (e < left) v[e] = Elem<DT>::widen(src[e]);
             }
             if (DT == GEMM_DTYPE_FP8F32 && in && left > 0) {
-                const float s = scale(r, k);
+                const float s = scale(r, k0 + k);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (e < left) v[e] *= s;
@@ -165,7 +165,7 @@ grouped_general_kernel(GroupedParams p, int tiles_m, int tiles_n) {
         }
     };
 
-    const int nk = (a.len + kBK - 1) / kBK;
+    const int nk = slabs_of(a.len, kBK);
     if (nk > 0) {
         a.fetch(0, scale_a);
         b.fetch(0, scale_b);

@@ -117,11 +117,12 @@ struct Loader {
     // cut the loop's schedule: a panel of 256 rows is below 2^31 bytes (checked on the host).
     __device__ __forceinline__ rsrc_t source(int t) const {
         const int step = (int)ld;
-        const int left = KN ? len - t * C::BK : len * esz - t * kSlab;          // KN: rows, else bytes
+        const int left = KN ? slab_left(t, C::BK, len) : len * esz - t * kSlab;          // KN: rows, else bytes
         const char *src = base + (KN ? (int64_t)t * C::BK * ld : (int64_t)t * kSlab);
         const int wide = ((KN ? rows * esz : max(left, 0)) + 15) & ~15;         // whole chunks
         const int deep = KN ? min(left, C::BK) : rows;
-        return make_rsrc(src, (uint32_t)(max(deep * step - (step - wide), 0) & ~((left - 1) >> 31)));
+        const int bytes = (int)((uint32_t)deep * (uint32_t)step - (uint32_t)(step - wide));      // past the end: any
+        return make_rsrc(src, (uint32_t)(max(bytes, 0) & ~((left - 1) >> 31)));
     }
     __device__ __forceinline__ void load(const rsrc_t &r, char *stage, int wave, int j) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + (j * C::NW + wave) * 1024), 16,
@@ -133,14 +134,13 @@ struct Loader {
     __device__ __forceinline__ void hold(int t, int set) {
         if constexpr (!C::DMA) {
             const int step = (int)ld, wide = (KN ? rows : len) * esz;
-            const int k0 = t * (KN ? C::BK : kSlab);                        // rows, or bytes of a row
-            const int first = KN ? min(k0, len - 1) : 0;
+            const int first = KN ? slab_first(t, C::BK, len) : 0;
             const int limit = KN ? slab_limit(len - first, C::BK, step, wide) : (rows - 1) * step + wide - 16;
             // From 16 bytes before: the last tile's columns may be fewer than a chunk.
             const char *src = base + (int64_t)first * ld - 16;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int at = min((int)offset(j) + row_of(j) * step + (KN ? byte_of(j) : k0), limit);
+                const int at = min((int)offset(j) + row_of(j) * step + (KN ? byte_of(j) : t * kSlab), limit);
                 reg[set][j] = reinterpret_cast<const Anywhere<u32x4> *>(src + (uint32_t)(at + 16))->v;
             }
         }
@@ -331,7 +331,7 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
     // (always, if it came through registers).
     const int len = a.len;
     const bool cut = !C::DMA || ((!C::AKN || !C::BKN) && len % C::BK != 0);
-    const int nk = cut ? (len - 1) / C::BK : (int)(((int64_t)len + C::BK - 1) / C::BK);
+    const int nk = cut ? (len - 1) / C::BK : slabs_of(len, C::BK);
 
     const int l32 = lane & 31;
     // Scales of the block that slab t is go to LDS as the slab does, into its
@@ -358,7 +358,7 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
         sc_bytes = of_a || of_b ? (uint32_t)((count - 1) * (int)each + 1) * 4u : 0u;
         sc_off = (uint32_t)min(of_a ? 64 * wave + lane : lane, count - 1) * (uint32_t)each * 4u;
     }
-    const int blocks = (int)(((int64_t)len + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK);
+    const int blocks = slabs_of(len, GEMM_SCALE_BLOCK);
     auto load_scales = [&](int t, float *set) __attribute__((always_inline)) {
         if constexpr (FP8) {
             const rsrc_t r = make_rsrc(sc_base + min(t, blocks - 1) * sc_step, sc_bytes);
