@@ -79,6 +79,32 @@ def test_norm_gradients(gpu_available):
     within(dw, want_dw, size_dw * (60 + depth(COLS) + 20) * U32, "dweight")          # sixty terms, and zeros
 
 
+def test_norm_gradients_of_long_rows(gpu_available):
+    """Rows past 2^27 values: a sum over partial rows for 32 columns a workgroup is more than 2^32 threads."""
+    M, N, edge = 2, 2 ** 27 + 40, 256
+    say(f"[large] norm gradients {M}x{N}")
+    g = gen(11)
+    host = [torch.randn(M, 2 * edge, generator=g).bfloat16() for _ in range(2)]
+    w0 = (1 + 0.1 * torch.randn(2 * edge, generator=g)).bfloat16()
+    s, dy = (torch.zeros(M, N, dtype=BF16, device="cuda") for _ in range(2))
+    w = torch.ones(N, dtype=BF16, device="cuda")
+    for t, h in ((s, host[0]), (dy, host[1]), (w, w0)):
+        t[..., :edge].copy_(h[..., :edge])
+        t[..., -edge:].copy_(h[..., edge:])
+    eps = 1e-5
+    dx, dw = tg.rms_norm_backward(dy, s, w, eps=eps)
+    a, d, up = f64(host[0]), f64(host[1]), f64(host[1]) * f64(w0)
+    rr = (a.square().sum(dim=1, keepdim=True) / N + eps) ** -0.5
+    mean = (up * a).sum(dim=1, keepdim=True) / N
+    want, size = rr * (up - a * rr * rr * mean), rr * (up.abs() + a.abs() * rr * rr * (up * a).abs().sum(1, True) / N)
+    got = torch.cat([dx[:, :edge], dx[:, -edge:]], dim=1)
+    # (A thread adds eight values of each end, zeros between them; then the tree.)
+    within(got, want, size * (2 * (16 + 26) + 16) * U32 + want.abs() * U16 * 1.001, "dx")
+    within(torch.cat([dw[:edge], dw[-edge:]]), (d * a * rr).sum(0), (d * a * rr).abs().sum(0) * (2 + 16 + 26 + 20) * U32,
+           "dweight")
+    assert not dx[:, edge:-edge].any() and not dw[edge:-edge].any()
+
+
 @pytest.mark.parametrize("op", ["T", "N"])
 def test_products_of_a_large_output(gpu_available, op):
     M, N, K = 65536 + 70, 32768, 144

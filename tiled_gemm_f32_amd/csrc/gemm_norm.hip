@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(1024)
 dweight_kernel(const float *partials, float *dweight, int parts, int64_t N) {
     __shared__ float part[32][32];
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 32 + c;
+    const int64_t col = folded_block() * 32 + c;
     float s[8] = {};
     if (col < N)
         for (int i = g; i < parts; i += 256) {
@@ -583,7 +583,7 @@ hipError_t launch_rms_norm_backward(const NormGradParams &p, hipStream_t s) {
     if (p.M > 0)
         err = p.dtype == GEMM_DTYPE_F32 ? grad_type<GEMM_DTYPE_F32>(p, s) : grad_type<GEMM_DTYPE_BF16F32>(p, s);
     if (err != hipSuccess || p.dweight == nullptr) return err;
-    return go(&dweight_kernel, dim3((unsigned)((p.N + 31) / 32)), 1024, s, (const float *)p.partials, p.dweight,
+    return go(&dweight_kernel, fold((p.N + 31) / 32), 1024, s, (const float *)p.partials, p.dweight,
               norm_grad_partials(p.M, p.N), p.N);
 }
 
