@@ -102,3 +102,59 @@ def test_refusals_are_the_wrappers(gpu_available, calls):
         tg.grouped_wgrad(x, x[:3], torch.tensor([4], dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         tg.grouped_wgrad(x, x, torch.tensor([4], dtype=torch.int32, device="cuda"), beta=1.0)
+
+
+def stream_of(t):
+    """The stream whose memory a tensor's is."""
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= t.data_ptr() < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+
+
+@pytest.mark.gpu
+def test_a_call_on_another_stream_allocates_there(gpu_available, calls):
+    """Memory of the current stream may still be in use there when the other stream writes it."""
+    g = torch.Generator().manual_seed(3)
+    x, w = torch.randn(96, 256, generator=g).cuda(), torch.ones(256, device="cuda")
+    qa, sa = tg.quantize(x)
+    qb, sb = tg.quantize(x, 128)
+    ends = torch.tensor([40, 96], dtype=torch.int32).cuda()
+    b = torch.randn(2, 64, 256, generator=g).cuda()
+    dy = torch.randn(96, 64, generator=g).cuda()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for call in (lambda h: tg.quantize(x, stream=h), lambda h: tg.quantize(x, 128, stream=h),
+                 lambda h: tg.rms_norm(x, w, residual=x, out_dtype=FP8, stream=h),
+                 lambda h: tg.rms_norm_backward(x, x, w, dsum=x, stream=h),
+                 lambda h: (tg.block_gemm(qa, qb, sa, sb, stream=h),),
+                 lambda h: (tg.grouped_gemm(x, b, ends, stream=h),),
+                 lambda h: (tg.grouped_wgrad(dy, x, ends, stream=h),)):
+        got = call(other.cuda_stream)
+        assert [stream_of(t) for t in got] == [other.cuda_stream] * len(got)
+        other.synchronize()
+        same(got, call(None) if len(got) > 1 else (call(None)[0],))
+    # the caller's own tensors stay its own
+    out, kept = torch.empty(96, 256, device="cuda"), torch.empty(96, 256, device="cuda")
+    got = tg.rms_norm(x, w, residual=x, out=out, summed=kept, stream=other.cuda_stream)
+    assert got[0] is out and got[1] is kept and got[2] is None
+    other.synchronize()
+    same(got[:2], tg.rms_norm(x, w, residual=x)[:2])
+
+
+@pytest.mark.gpu
+def test_results_of_another_stream_may_be_dropped_on_the_current_one(gpu_available, calls):
+    """While the current stream still has work, memory of a result that was dropped is not given to the other stream."""
+    x = torch.ones(1024, 1024, device="cuda")
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    q, s = tg.quantize(x, stream=other.cuda_stream)
+    other.synchronize()
+    where = q.data_ptr()
+    torch.cuda._sleep(20_000_000)
+    use = q.view(torch.uint8).clone()
+    del q
+    with torch.cuda.stream(other):
+        again = torch.empty(1024, 1024, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() != where
+    torch.cuda.synchronize()
+    assert (use == use[0, 0]).all()

@@ -8,9 +8,11 @@ is not passed in, and forward to the C entry points of include/gemm.h, which
 states each operator's formula.  Tensors are 2-D (or 3-D: a group's matrix
 each) with unit stride along their last dimension; rows may be padded.  Work
 goes to ``stream`` (an integer handle; None: torch's current stream) and no
-call waits for the device.  What a call allocates belongs to torch's current
-stream; with another ``stream`` it is recorded there too, so that its memory
-is not reused before the work is done.
+call waits for the device.  What a call allocates belongs to the stream that
+it runs on, so that the memory's earlier uses are over when the call writes
+it; results made on another stream than torch's current one are recorded on
+that one too, so that they may be used and dropped there once the caller has
+ordered the two.
 """
 from __future__ import annotations
 
@@ -54,6 +56,23 @@ def _common(name: str, *args):
     got = getattr(_calls, name)(*args, device, _stream_of_calls(device))
     if type(got) is int:
         raise GemmError(got, name)
+    return got
+
+
+def _elsewhere(stream: int, like, fn, *args):
+    """fn(*args) with `stream` as torch's current one, or None if it is that already (or `like` not on a GPU)."""
+    import torch
+    if not like.is_cuda:
+        return None
+    device = like.get_device()
+    if stream == torch._C._cuda_getCurrentRawStream(device):
+        return None
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        got = fn(*args)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and not any(t is a for a in args):
+            t.record_stream(caller)
     return got
 
 
@@ -121,16 +140,10 @@ def _new(rows: int, cols: int, dtype, device, unit: int = 1):
     return torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device), ld
 
 
-def _call(name: str, device: int, stream, made, fn, *args):
-    """fn(*args, stream) on GPU `device`; tensors in `made` were allocated for this call."""
+def _call(name: str, device: int, fn, *args):
+    """fn(*args, stream) on GPU `device`, on its current stream."""
     import torch
-    current = torch._C._cuda_getCurrentRawStream(device)
-    if stream is None:
-        stream = current
-    elif stream != current:
-        other = torch.cuda.ExternalStream(stream, device=device)
-        for t in made:
-            t.record_stream(other)
+    stream = torch._C._cuda_getCurrentRawStream(device)
     if torch._C._cuda_getDevice() == device:
         st = fn(*args, stream)
     else:
@@ -152,26 +165,27 @@ def quantize(x, block_rows: int = 1, out=None, scales=None, stream=None):
         got = _common("quantize", x, block_rows)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, x, quantize, x, block_rows, out, scales)
+        if got is not None:
+            return got
     dt = _float_type(x, "x")
     device = _device(x, "x")
     _check(x, "x", device)
     if block_rows not in (1, GEMM_SCALE_BLOCK):
         raise ValueError(f"block_rows is 1 or {GEMM_SCALE_BLOCK} (got {block_rows})")
     M, K = x.shape
-    made = []
     if out is None:
         out, ldq = _new(M, K, torch.float8_e4m3fn, x.device, 16)
-        made.append(out)
     else:
         _check(out, "out", device, (M, K), torch.float8_e4m3fn)
         ldq = _ld(out, "out")
     if scales is None:
         scales, lds = _new(-(-M // block_rows), _blocks(K), torch.float32, x.device)
-        made.append(scales)
     else:
         _check(scales, "scales", device, (-(-M // block_rows), _blocks(K)), torch.float32)
         lds = _ld(scales, "scales")
-    _call("quantize", device, stream, made, gemm_quantize, dt, block_rows, M, K, x.data_ptr(), _ld(x, "x"),
+    _call("quantize", device, gemm_quantize, dt, block_rows, M, K, x.data_ptr(), _ld(x, "x"),
           out.data_ptr(), ldq, scales.data_ptr(), lds)
     return out, scales
 
@@ -191,6 +205,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
         got = _common("rms_norm", x, weight, residual, eps, out_dtype)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, x, rms_norm, x, weight, residual, eps, out_dtype, out, summed, scales)
+        if got is not None:
+            return got
     dt = _float_type(x, "x")
     device = _device(x, "x")
     _check(x, "x", device)
@@ -198,7 +216,6 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
     _check(weight, "weight", device, (N,), x.dtype)
     if N > 1 and weight.stride(0) != 1:
         raise ValueError("weight must be contiguous")
-    made = []
     r_ptr = s_ptr = c_ptr = ldr = ld_sum = ld_scales = 0
     if residual is not None:
         _check(residual, "residual", device, (M, N), x.dtype)
@@ -208,7 +225,6 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
         s_ptr, ld_sum = summed.data_ptr(), _ld(summed, "summed")
     elif residual is not None:
         summed, ld_sum = _new(M, N, x.dtype, x.device)
-        made.append(summed)
         s_ptr = summed.data_ptr()
     if out is not None:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -219,18 +235,16 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, out=No
     else:
         kind = _out_type(out_dtype or x.dtype, "out")
         out, ldo = _new(M, N, out_dtype or x.dtype, x.device, 16 if kind == GEMM_OUT_FP8 else 1)
-        made.append(out)
     if kind == GEMM_OUT_FP8:
         if scales is None:
             scales, ld_scales = _new(M, _blocks(N), torch.float32, x.device)
-            made.append(scales)
         else:
             _check(scales, "scales", device, (M, _blocks(N)), torch.float32)
             ld_scales = _ld(scales, "scales")
         c_ptr = scales.data_ptr()
     elif scales is not None:
         raise ValueError("scales go with a float8_e4m3fn output")
-    _call("rms_norm", device, stream, made, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"), r_ptr, ldr,
+    _call("rms_norm", device, gemm_rms_norm, dt, M, N, x.data_ptr(), _ld(x, "x"), r_ptr, ldr,
           weight.data_ptr(), float(eps), s_ptr, ld_sum, kind, out.data_ptr(), ldo, c_ptr, ld_scales)
     return out, summed if summed is not None else x, scales
 
@@ -248,6 +262,10 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
         got = _common("rms_norm_backward", dy, summed, weight, dsum, eps)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, dy, rms_norm_backward, dy, summed, weight, dsum, eps, dx, want_dweight)
+        if got is not None:
+            return got
     dt = _float_type(dy, "dy")
     device = _device(dy, "dy")
     _check(dy, "dy", device)
@@ -258,10 +276,8 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
         raise ValueError("weight must be contiguous")
     if dsum is not None:
         _check(dsum, "dsum", device, (M, N), dy.dtype)
-    made = []
     if dx is None:
         dx, lddx = _new(M, N, dy.dtype, dy.device)
-        made.append(dx)
     else:
         _check(dx, "dx", device, (M, N), dy.dtype)
         lddx = _ld(dx, "dx")
@@ -271,9 +287,8 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
         need = gemm_rms_norm_workspace_size(M, N)
         dweight = torch.empty_strided((N,), (1,), dtype=torch.float32, device=dy.device)
         ws = torch.empty_strided((max(need, 4),), (1,), dtype=torch.uint8, device=dy.device)
-        made += [dweight, ws]
         dw_ptr, ws_ptr = dweight.data_ptr(), ws.data_ptr()
-    _call("rms_norm_backward", device, stream, made, gemm_rms_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
+    _call("rms_norm_backward", device, gemm_rms_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
           summed.data_ptr(), _ld(summed, "summed"), weight.data_ptr(), float(eps),
           dsum.data_ptr() if dsum is not None else 0, _ld(dsum, "dsum") if dsum is not None else 0, dx.data_ptr(), lddx,
           dw_ptr, ws_ptr, need)
@@ -306,7 +321,7 @@ def _block_scales(A, B, a_scales, b_scales, op_b: str, M: int, N: int, K: int, d
                        b_scales.stride(0) if lead else 0)
 
 
-def _product_out(M: int, N: int, out, out_dtype, default, like, device: int, made):
+def _product_out(M: int, N: int, out, out_dtype, default, like, device: int):
     """(out, its leading dimension, its type) of a product."""
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -317,7 +332,6 @@ def _product_out(M: int, N: int, out, out_dtype, default, like, device: int, mad
         _check(out, "out", device, (M, N))
         return out, _ld(out, "out"), kind
     out, ldo = _new(M, N, out_dtype or default, like.device)
-    made.append(out)
     return out, ldo, kind
 
 
@@ -334,6 +348,10 @@ def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, ou
         got = _common("block_gemm", A, B, a_scales, b_scales, op_b, alpha, out_dtype)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, A, block_gemm, A, B, a_scales, b_scales, op_b, alpha, out, out_dtype)
+        if got is not None:
+            return got
     if op_b not in ("N", "T"):
         raise ValueError("op_b is 'N' or 'T'")
     device = _device(A, "A")
@@ -344,9 +362,8 @@ def block_gemm(A, B, a_scales, b_scales, op_b: str = "T", alpha: float = 1.0, ou
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, op_b={op_b} {tuple(B.shape)}")
     sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K, device)
-    made = []
-    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device, made)
-    _call("block_gemm", device, stream, made, gemm_block_scaled, GEMM_OP_T if op_b == "T" else GEMM_OP_N, M, N, K,
+    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device)
+    _call("block_gemm", device, gemm_block_scaled, GEMM_OP_T if op_b == "T" else GEMM_OP_N, M, N, K,
           float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), sc, kind, out.data_ptr(), ldo)
     return out
 
@@ -373,6 +390,10 @@ def grouped_gemm(A, B, ends, a_scales=None, b_scales=None, op_b: str = "T", alph
         got = _common("grouped_gemm", A, B, ends, a_scales, b_scales, op_b, alpha, out_dtype)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, A, grouped_gemm, A, B, ends, a_scales, b_scales, op_b, alpha, out, out_dtype)
+        if got is not None:
+            return got
     if op_b not in ("N", "T"):
         raise ValueError("op_b is 'N' or 'T'")
     fp8 = A.dtype == torch.float8_e4m3fn
@@ -391,9 +412,8 @@ def grouped_gemm(A, B, ends, a_scales=None, b_scales=None, op_b: str = "T", alph
         sc = _block_scales(A, B, a_scales, b_scales, op_b, M, N, K, device)
     elif a_scales is not None or b_scales is not None:
         raise ValueError("scales go with float8_e4m3fn operands")
-    made = []
-    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A, device, made)
-    _call("grouped_gemm", device, stream, made, gemm_grouped, dt, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
+    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16 if fp8 else A.dtype, A, device)
+    _call("grouped_gemm", device, gemm_grouped, dt, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
           ends.data_ptr(), M, N, K, float(alpha), A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
           B.stride(0) if groups > 1 else 0, sc, kind, out.data_ptr(), ldo)
     return out
@@ -410,6 +430,10 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
         got = _common("grouped_wgrad", dy, x, ends, alpha)
         if got is not None:
             return got
+    if stream is not None:
+        got = _elsewhere(stream, dy, grouped_wgrad, dy, x, ends, alpha, beta, out)
+        if got is not None:
+            return got
     dt = _float_type(dy, "dy")
     device = _device(dy, "dy")
     _check(dy, "dy", device)
@@ -422,14 +446,12 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
         raise ValueError(f"ends must be 1-D, got shape {tuple(ends.shape)}")
     groups = ends.shape[0]
     _check_ends(ends, device, groups)
-    made = []
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs an input out")
         out = torch.empty((groups, N, K), dtype=torch.float32, device=dy.device)
-        made.append(out)
     _check(out, "out", device, (groups, N, K), torch.float32)
-    _call("grouped_wgrad", device, stream, made, gemm_grouped_wgrad, dt, groups, ends.data_ptr(), M, N, K,
+    _call("grouped_wgrad", device, gemm_grouped_wgrad, dt, groups, ends.data_ptr(), M, N, K,
           float(alpha), dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), float(beta), out.data_ptr(),
           _ld(out, "out"), out.stride(0) if groups > 1 else 0)
     return out
