@@ -23,6 +23,7 @@ import os
 import re
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -179,7 +180,20 @@ def resource_markdown(table: dict) -> str:
     return "\n".join(out) + "\n"
 
 
-def build_torch_calls() -> None:
+def build_torch_calls() -> bool:
+    """Build _torch_calls.so; where torch, its or Python's headers, or g++ are missing, warn and go on
+    without it: the C library needs none of them, and the torch wrappers then take every call themselves."""
+    try:
+        _compile_torch_calls()
+        return True
+    except (ImportError, OSError, RuntimeError) as err:
+        if os.path.exists(CALLS_PATH):
+            os.remove(CALLS_PATH)              # of other sources
+        warnings.warn(f"_torch_calls.so was not built, the torch wrappers' calls will take the host longer: {err}")
+        return False
+
+
+def _compile_torch_calls() -> None:
     """Compile _torch_calls.so, the torch wrappers' common calls (host code only).  The torch
     libraries it names are those of the process that imports it, which has loaded torch first."""
     import sysconfig
