@@ -767,6 +767,16 @@ struct TileChoice {
     double time;
 };
 
+// Time of `turns` turns of tiles that are `slabs` slabs deep.  tile_factor: of a tile's own time; `matrix`: us of
+// matrix instructions that a slab of 128 x 128 takes, where they take longer than its loads (fp32);
+// `staged`: us that a lone workgroup's slab takes longer through registers, a busy one's half as much.
+inline double tile_time(const TileCost &c, double turns, double slabs, double tile_factor, double matrix,
+                        double staged) {
+    const double least_slab = matrix * c.bm * c.bn / (128 * 128);
+    return std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
+                    slabs * (std::max(c.alone, least_slab) + staged) + 6.0);
+}
+
 // The tile of the least time over `rows` rows of an output of `cols` columns,
 // `slabs` slabs deep, in `groups` groups: large ones move the fewest bytes a
 // product (2048 x 4096 x 4096 fp8: 42 us in 128 x 256, 50 in 128 x 128, 57
@@ -775,14 +785,10 @@ struct TileChoice {
 // rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128; 8 groups of 8192
 // x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).
 // Groups are taken to be alike, with half an empty tile each at their ends.
-// `first`: the largest to consider; `matrix`: us of matrix instructions that
-// a slab of 128 x 128 takes, where they take longer than its loads (fp32);
-// `staged`: us that a lone workgroup's slab takes longer through registers, a
-// busy one's half as much; `share`: 256 x 256 tiles past the last whole turn
-// go to two or four workgroups each.
-inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first,
-                              double tile_factor = 1.0, double matrix = 0.0, double staged = 0.0,
-                              bool share = false) {
+// `first`: the largest to consider.  256 x 256 tiles past the last whole turn go to two or four
+// workgroups each.
+inline TileChoice tile_choice(double rows, double cols, double slabs, double groups, TileSize first, double matrix,
+                              double staged) {
     TileChoice best = {};
     double least = 0.0;
     for (int i = first; i <= kTile32; ++i) {
@@ -791,10 +797,8 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
         const double high = groups > 1 ? groups * std::max(1.0, each) : std::ceil(rows / c.bm);
         const double tiles = high * std::ceil(cols / c.bn);
         const double turns = std::ceil(tiles / kComputeUnits);
-        const double least_slab = matrix * c.bm * c.bn / (128 * 128);
-        double t = std::max(turns * (slabs * (std::max(c.slab, least_slab) + staged / 2) + c.tile * tile_factor),
-                                  slabs * (std::max(c.alone, least_slab) + staged) + 6.0);
-        if (share && i == kTile256) {
+        double t = tile_time(c, turns, slabs, 1.0, matrix, staged);
+        if (i == kTile256) {
             const double whole = std::floor(tiles / kComputeUnits), left = tiles - kComputeUnits * whole;
             const double rest = left <= 0.0                  ? 0.0
                                 : left <= kComputeUnits / 4 ? slabs * 0.65 + 6.0
@@ -833,8 +837,7 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
     // registers: 233 us in 128 x 128, 185 in 192 x 256.)
     constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
-    const TileChoice c =
-        tile_choice(p.M, p.N, slabs, groups, first, 1.0, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15, true);
+    const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15);
     constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
     if (deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6) < c.time &&
         deep_takes(DT, op, DMA, p))
@@ -872,25 +875,44 @@ template <int DT> hipError_t launch_typed(int32_t op_b, bool dma, const GroupedP
 
 
 // Weight gradients: both operands are walked down their rows.  Results are
-// fp32, so a tile's store takes twice the time.
+// fp32, so a tile's store takes twice the time.  Every group has all N x K of
+// them, so a group's row tiles are counted as they are.  Three workgroups of
+// 64 x 128 share a compute unit, so part of a turn of those costs a part.
+// (6953 rows in 3 groups of 632 x 2136 bf16: 52 us in 256 x 256, 37 in 128 x 128;
+// 4096 in 4 of 512 x 1024: 16.4 in 128 x 128, 11.8 in 64 x 128; 411 in 8 of
+// 400 x 728, 1.3 turns of 64 x 128: 6.8 and 6.0.  Over 180 sizes of 250 to 16384
+// rows the tile taken is 1.3% slower than the best of the three, 15% at most but
+// for five.)
+inline TileSize wgrad_tile(int N, int K, int groups, double slabs, bool large, double matrix) {
+    constexpr TileSize sizes[] = {kTile256, kTile128, kTile64};        // what launch_wgrad has
+    TileSize best = kTile64;
+    double least = 0.0;
+    for (const TileSize size : sizes) {
+        if (size == kTile256 && !large) continue;
+        const TileCost &c = kTileCosts[size];
+        const double tiles = groups * std::ceil((double)N / c.bm) * std::ceil((double)K / c.bn);
+        const double turns = tiles / kComputeUnits;
+        const double t =
+            tile_time(c, size == kTile64 ? std::max(1.0, turns) : std::ceil(turns), slabs, 2.0, matrix, 0.0);
+        if (least == 0.0 || t < least) {
+            least = t;
+            best = size;
+        }
+    }
+    return best;
+}
 template <int DT> hipError_t launch_wgrad(bool dma, const GroupedParams &p, hipStream_t s) {
     constexpr bool F32 = DT == GEMM_DTYPE_F32;
-    // The outputs of all groups together, each as deep as a group has rows.
+    // Each group as deep as they are on average.
     const double slabs = std::ceil((double)p.M / p.groups / (F32 ? 32 : 64));
-    switch (tile_choice((double)p.N * p.groups, p.K, slabs, p.groups, dma && !F32 ? kTile256 : kTile128, 2.0,
-                        F32 ? kMatrixF32 : 0.0).size) {
-        case kTile256:
-        case kTile192:
-        case kTileWide:
-            if constexpr (!F32)
-                if (dma) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s);
-        case kTile128:
-            return dma ? launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, true>>(p, s)
-                       : launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, false>>(p, s);
-        default:
-            return dma ? launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, true>>(p, s)
-                       : launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, false>>(p, s);
-    }
+    const TileSize size = wgrad_tile(p.N, p.K, p.groups, slabs, dma && !F32, F32 ? kMatrixF32 : 0.0);
+    if constexpr (!F32)
+        if (size == kTile256) return launch_grouped_tile<TileConfig<DT, 4, 2, 2, 4, true, true, true>>(p, s);
+    if (size == kTile128)
+        return dma ? launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, true>>(p, s)
+                   : launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, true, true, false>>(p, s);
+    return dma ? launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, true>>(p, s)
+               : launch_grouped_tile<TileConfig<DT, 1, 2, 2, 2, true, true, false>>(p, s);
 }
 
 }  // namespace
