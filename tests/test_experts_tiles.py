@@ -199,6 +199,12 @@ def test_weight_gradients_of_every_tile(gpu_available, dtype, M, groups, N, K):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,groups,N,K", [(1800, 3, 632, 2136), (300, 8, 256, 1912)])
+def test_weight_gradients_of_128_x_128_tiles(gpu_available, dtype, M, groups, N, K):
+    test_weight_gradients_of_every_tile(gpu_available, dtype, M, groups, N, K)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_weight_gradients_of_rows_far_apart(gpu_available, dtype):
     M, N, K = 35, 70, 65
     say(f"[wgrad far] {dtype}")
