@@ -572,7 +572,9 @@ GEMM_API gemm_status gemm_block_scaled(int32_t op_b, int64_t M, int64_t N, int64
  *
  *     dW_g[n][k] = alpha * sum over rows i of group g of dY[i][n] * X[i][k] + beta * dW_g[n][k]
  *
- * at dW + g*stride_w (row n at n*ldw).  A group without rows gives beta * dW
+ * at dW + g*stride_w (row n at n*ldw), groups' results one after the other
+ * or their rows in turn (stride_w >= K, ldw >= (groups - 1)*stride_w + K), never
+ * over one another.  A group without rows gives beta * dW
  * (zeros when beta == 0, whatever dW held).  Rows from the last end on are
  * not read.
  */

@@ -399,6 +399,23 @@ def test_grouped_wgrad(gpu_available, dtype, sizes, rest, N, K):
                 at += size
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,K", [(70, 33), (300, 256), (1, 40), (40, 3)])
+def test_weight_gradients_into_rows_in_turn(gpu_available, dtype, N, K):
+    """out as N x groups x K in memory: a row of every group after the other, with a gap that stays as it was."""
+    say(f"[wgrad] rows in turn {dtype} {N}x{K}")
+    G, M = 3, 100
+    dy, x = torch.randn(M, N, generator=gen(1)).to(dtype).cuda(), torch.randn(M, K, generator=gen(2)).to(dtype).cuda()
+    ends = ends_of([30, 0, 70]).cuda()
+    buf = torch.full((N, G, K + 5), 7.0, device="cuda")
+    out = buf[:, :, :K].transpose(0, 1)
+    want = tg.grouped_wgrad(dy, x, ends)
+    assert tg.grouped_wgrad(dy, x, ends, out=out) is out and torch.equal(out, want)
+    tg.grouped_wgrad(dy, x, ends, beta=1.0, out=out)
+    assert torch.equal(out, tg.grouped_wgrad(dy, x, ends, beta=1.0, out=want))
+    assert (buf[:, :, K:] == 7.0).all()
+
+
 def test_grouped_gradients_against_differences(gpu_available):
     """The three products of a training step, as gradients of one loss."""
     say("[grouped] differences")

@@ -105,6 +105,14 @@ def test_calls_outside_what_the_kernels_index_are_unsupported(fn, kwargs):
     assert fn(**kwargs) == UNSUP
 
 
+@pytest.mark.parametrize("ldw,stride,fine", [
+    (128, 256 * 128, True), (3 * 128, 128, True), (400, 130, True), (128, 255 * 128 + 127, False), (3 * 128 - 1, 128, False),
+    (400, 127, False), (128, 128, False), (128, 0, False), (2 ** 31 - 1, 2 ** 30, False), (128, 2 ** 62, True),
+    (400, 2 ** 47, True)])
+def test_results_of_groups_may_take_turns_but_not_overlap(ldw, stride, fine):
+    assert (wgrad(ldw=ldw, stride=stride) == INVALID) == (not fine)
+
+
 @pytest.mark.parametrize("fn,kwargs", [
     (quant, dict(M=0, X=0, Q=0, s=0)), (quant, dict(K=0, X=0, Q=0, s=0)), (norm, dict(M=0, X=0, w=0, out=0)),
     (norm, dict(N=0, X=0, w=0, out=0)), (grad, dict(M=0, dY=0, S=0, w=0, dX=0)), (grad, dict(N=0, dY=0, S=0, dX=0)),

@@ -140,8 +140,6 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
     const bool writes = groups > 0 && N > 0 && K > 0;
     const bool reads = writes && M > 0 && alpha != 0.0f;
     if (writes && (bad_ptr(dW, 4) || bad_ptr(ends, 4))) return GEMM_ERR_INVALID_ARG;
-    // Groups' results must not overlap.
-    if (writes && groups > 1 && stride_w < (N - 1) * ldw + K) return GEMM_ERR_INVALID_ARG;
     const uintptr_t esz = size_of(dtype);
     if (reads && (bad_ptr(dY, esz) || bad_ptr(X, esz))) return GEMM_ERR_INVALID_ARG;
     if (!float_type(dtype)) return GEMM_ERR_UNSUPPORTED;
@@ -149,6 +147,11 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
         groups > kMaxGroups || ceil_div(N, 64) * ceil_div(K, 64) > kMaxTiles)
         return GEMM_ERR_UNSUPPORTED;
     if (!writes) return GEMM_OK;
+    // Groups' results must not overlap: each starts past the one before, or row n of all of them lies
+    // before row n + 1 of the first.
+    const bool apart = stride_w >= (N - 1) * ldw + K;
+    const bool between = stride_w >= K && stride_w <= ldw && (groups - 1) * stride_w + K <= ldw;
+    if (groups > 1 && !apart && !between) return GEMM_ERR_INVALID_ARG;
     gemm_status st = gemm::check_device();
     if (st != GEMM_OK) return st;
     gemm::GroupedParams p = {};
