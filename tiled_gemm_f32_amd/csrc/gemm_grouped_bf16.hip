@@ -5,7 +5,8 @@
 namespace gemm {
 namespace {
 
-// The others are made as the launchers below name them.
+// One kernel by name, so that this source shows which template it makes (and counts among those whose
+// kernels the resource table has to list); the launchers below make the others.
 template __global__ void grouped_tile_kernel<TileConfig<GEMM_DTYPE_BF16F32, 3, 2, 2, 4, false, false, true>>(GroupedParams, int, int);
 
 }  // namespace

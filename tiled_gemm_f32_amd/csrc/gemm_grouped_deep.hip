@@ -13,9 +13,13 @@
 // instead of two, were no faster at 256 tiles and slower at more: 1000 x 512 x
 // 4096 bf16, 512 tiles, 17.4 us, 15.2 so.)
 //
-// 128 x 2000 x 8000 fp8 10.2 us (16 MB of weights: 1.6 TB/s, bound by the
-// latency of eight slabs a wave); 16 x 4096 x 4096 fp8 against K x N weights
-// 9.3 us; 64 x 1000 x 1024 fp32 9 us, 3.5 of them matrix instructions.
+// On inputs that change from call to call: 128 x 2000 x 8000 fp8 12.0 us (16 MB
+// of weights: 1.3 TB/s, bound by the latency of eight slabs a wave; 11 where
+// the caches hold the weights); 16 x 4096 x 4096 fp8 against K x N weights 13.5
+// us (9.9), 16 x 8192 x 8192 24 us: a workgroup for each 128 columns, which is
+// none for most compute units; 64 rows over 32 experts of 4096 x 4096 fp8, K x
+// N, 21 of them with rows, 72 us (4.9 TB/s); 64 x 1000 x 1024 fp32 7.8 us, 3.5 of
+// them matrix instructions.
 //
 // Loads, layouts and fragments are those of gemm_grouped_tile.hpp with one
 // wave.  fp8: the products of the two block scales are made once a workgroup,

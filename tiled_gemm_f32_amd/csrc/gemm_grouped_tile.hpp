@@ -10,13 +10,18 @@
 // wave and the reads of A fragment i + 1 (or of the next slab) run under the
 // products of fragment i.
 //
-// Measured, and what bounds it: 8192^3 fp8 in 256 x 256 takes 470 to 500 us
-// (2.2 to 2.35 PF): a slab takes 1.6 us, of which its matrix instructions
-// alone would take 0.93 and its 64 KB 0.55 to 0.68 to land with every
-// compute unit loading.  8 groups of 8192 x 4096 x 2048 bf16: 138 us (1.0 PF;
-// a matrix product of 8192^3 reaches 1.1 to 1.5 here), bound by the power
-// limit on random data and by the last turn of tiles.  fp32 is bound by the
-// matrix cores (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads).
+// Measured, and what bounds it: 8192^3 fp8 in 256 x 256 takes 455 to 500 us
+// over boxes (2.2 to 2.4 PF; profiled, 484 at least and 594 in the median): a
+// slab takes 1.6 us, of which its matrix instructions alone would take 0.93
+// and its 64 KB 0.55 to 0.68 to land with every compute unit loading.  8
+// uneven groups of 8192 x 4096 x 2048 bf16, inputs changing from call to call:
+// 165 us (0.83 PF; a library's product of 8192^3 reaches 1.1 to 1.5 here).
+// The matrix cores are 0.47 busy in it: 353 MB come for operands of 168, a
+// wave's tile of 128 x 64 reads more of LDS than 128 x 128 would, a workgroup
+// stores its tile with the matrix cores idle, and groups cut tiles.  It is not
+// the power limit: zeros take 161.  fp32 is bound by the matrix cores, 0.84 to
+// 0.87 busy (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads; 8 uneven
+// groups of 8192 x 2048 x 1024 285 us, 121 TF; 8192 x 4096 x 4096 1.88 ms, 146).
 //
 // fp8 with block scales: the matrix core sums a block of 128 k into a partial
 // tile of its own (two v_mfma_f32_32x32x64_f8f6f4, the first with a zero
@@ -779,11 +784,14 @@ inline double tile_time(const TileCost &c, double turns, double slabs, double ti
 
 // The tile of the least time over `rows` rows of an output of `cols` columns,
 // `slabs` slabs deep, in `groups` groups: large ones move the fewest bytes a
-// product (2048 x 4096 x 4096 fp8: 42 us in 128 x 256, 50 in 128 x 128, 57
-// in 256 x 256, which leaves half of the compute units idle; 8192^3: 560,
-// 600 and 520 us; 16 groups of 8192 x 4096 x 4096: 225, 235 and 195 us; 64
-// rows of 4096 x 4096: 29, 25 and 45 us, but 14 in 32 x 128; 8 groups of 8192
-// x 4096 x 2048 bf16, 2.3 turns of 256 x 256: 155, and 138 us in 192 x 256).
+// product.  In 128 x 256, 128 x 128 and 256 x 256 (these with their last turn
+// shared out), us: 2048 x 4096 x 4096 fp8 39, 43 and 42; 8192^3 510, 586 and
+// 458; 16 uneven groups of 8192 x 4096 x 4096 210 to 220, 229 to 240 and 175 to
+// 183; 64 rows of 4096 x 4096 27, 23 and 26, but 13 in 32 x 128.  192 x 256 is
+// for numbers of tiles that 256 x 256 makes a poor last turn of: 32 uneven
+// groups of 8192 x 2048 x 1024 bf16 66 to 69, and 69 to 72 in 256 x 256; the
+// estimate takes it for 8 uneven groups of 8192 x 4096 x 2048 too, 164 to 172
+// where 256 x 256 takes 153 to 163.
 // Groups are taken to be alike, with half an empty tile each at their ends.
 // `first`: the largest to consider.  256 x 256 tiles past the last whole turn go to two or four
 // workgroups each.
@@ -816,9 +824,10 @@ inline TileChoice tile_choice(double rows, double cols, double slabs, double gro
 
 // Time of the kernel whose waves share out k (gemm_grouped_deep.hip) in tiles of 32 x bn: `each` us
 // for a wave's slab, eight slabs at a time.  Tiles of 32 columns share a compute unit by two, others
-// take it in turns; groups are unlike each other, so a tenth is added to the number of tiles.  (16 x 4096
-// x 4096 fp8 against K x N weights: 12.1 us in 32 x 128, 9.3 so; 128 x 2000 x 8000 fp8: 21.8 and
-// 10.2; 64 x 1000 x 1024 fp32: 21.4 and 9; but 300 x 2000 x 4000 fp8, 630 tiles: 14.6 and 19.8.)
+// take it in turns; groups are unlike each other, so a tenth is added to the number of tiles.  (On the
+// same inputs in every call, 16 x 4096 x 4096 fp8 against K x N weights: 13.0 us in 32 x 128, 9.9 so;
+// 128 x 2000 x 8000 fp8: 23.2 and 11.3; 64 x 1000 x 1024 fp32: 21.4 and 8.1; but 300 x 2000 x 4000 fp8,
+// 630 tiles: 15.8 and 17.3.)
 inline double deep_time(double rows, double cols, double slabs, double groups, int bn, double each) {
     const double high = groups > 1 ? 1.1 * groups * std::max(1.0, rows / groups / 32 + 0.5) : std::ceil(rows / 32);
     const double tiles = high * std::ceil(cols / bn);
@@ -835,7 +844,7 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     const double groups = p.ends != nullptr ? std::max(1, std::min(p.groups, p.M)) : 1;
     // Staging registers leave room for fewer accumulators, partial tiles for fewer still; fp32 is
     // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
-    // registers: 233 us in 128 x 128, 185 in 192 x 256.)
+    // registers: 217 us in 128 x 128, 187 in 192 x 256.)
     constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
     const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15);
     constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
