@@ -158,3 +158,21 @@ def test_results_of_another_stream_may_be_dropped_on_the_current_one(gpu_availab
     assert again.data_ptr() != where
     torch.cuda.synchronize()
     assert (use == use[0, 0]).all()
+
+
+@pytest.mark.gpu
+def test_the_default_streams_handle_is_the_default_stream(gpu_available, calls):
+    """Handle 0 while another stream is the current one: the call runs behind the default stream's work."""
+    x = torch.zeros(512, 512, device="cuda")
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(20_000_000)
+            x.fill_(3.0)
+        q, s = tg.quantize(x, stream=default.cuda_stream)
+        torch.cuda.current_stream().wait_stream(default)
+        assert stream_of(q) == stream_of(s) == default.cuda_stream == 0
+        assert (q.float() == 448.0).all()
+        # (Divided on the host: torch on the GPU multiplies by the rounded reciprocal.)
+        assert (s.cpu() == torch.tensor(3.0) / 448.0).all()

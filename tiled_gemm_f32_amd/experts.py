@@ -68,7 +68,9 @@ def _elsewhere(stream: int, like, fn, *args):
     if stream == torch._C._cuda_getCurrentRawStream(device):
         return None
     caller = torch.cuda.current_stream(device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+    # (torch takes a handle of 0, the default stream, for none given, and makes a stream.)
+    other = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(other):
         got = fn(*args)
     for t in got if isinstance(got, tuple) else (got,):
         if t is not None and not any(t is a for a in args):
