@@ -260,7 +260,8 @@ typedef enum gemm_activation {
 typedef enum gemm_output {
     GEMM_OUT_F32 = 0,        /* fp32, to C */
     GEMM_OUT_BF16 = 1,       /* bfloat16 bit patterns, to out */
-    GEMM_OUT_FP8 = 2         /* OCP E4M3 bytes, saturating, to out */
+    GEMM_OUT_FP8 = 2,        /* OCP E4M3 bytes, saturating, to out */
+    GEMM_OUT_INT8 = 3        /* 8-bit integers with a scale a row; gemm_layer_norm only */
 } gemm_output;
 
 typedef struct gemm_epilogue {
@@ -589,6 +590,171 @@ GEMM_API gemm_status gemm_grouped_wgrad(int32_t dtype, int32_t groups, const int
                                         const void *dY, int64_t lddy, const void *X, int64_t ldx,
                                         float beta, float *dW, int64_t ldw, int64_t stride_w,
                                         gemm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the experts: layer norm, 8-bit integer products, and tokens sorted
+ * by expert and back.  The rules of the calls above hold here too.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Layer norm over rows of N values, with the residual's addition.
+ *
+ *     s = round(x + residual)                          (x, if residual is NULL)
+ *     y = (s - mean) * (mean of (s - mean)^2 + eps)^-1/2 * weight + bias
+ *
+ * the means over the row, both sums fp32 and the second one of the
+ * differences.  Arguments, types, rounding of s and what may be passed in
+ * place are those of gemm_rms_norm; bias (N values of type dtype) may be
+ * NULL (zero).  out_type GEMM_OUT_FP8 gives codes with a scale for every 128
+ * columns as there; GEMM_OUT_INT8 gives 8-bit integers with one scale a row,
+ * scales[i*ld_scales], as gemm_quantize_int8 does of y before any rounding.
+ */
+GEMM_API gemm_status gemm_layer_norm(int32_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx,
+                                     const void *residual, int64_t ldr, const void *weight, const void *bias,
+                                     float eps, void *sum, int64_t ld_sum, int32_t out_type, void *out, int64_t ldo,
+                                     float *scales, int64_t ld_scales, gemm_stream_t stream);
+
+/*
+ * Gradients of gemm_layer_norm, as gemm_rms_norm_backward takes and gives
+ * them.  With r = (mean of (s - mean)^2 + eps)^-1/2 of a row, n = (s - mean) * r
+ * and g = dy * weight:
+ *
+ *     dX = r * (g - mean(g) - n * mean(g * n)) + dS     (of X and of the residual)
+ *     dweight[j] = sum over rows of dy * n              (fp32)
+ *     dbias[j] = sum over rows of dy                    (fp32)
+ *
+ * dweight and dbias may each be NULL (not wanted); unless both are,
+ * `workspace` holds gemm_layer_norm_workspace_size(M, N) bytes.
+ */
+GEMM_API int64_t gemm_layer_norm_workspace_size(int64_t M, int64_t N);
+GEMM_API gemm_status gemm_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, int64_t lddy,
+                                              const void *S, int64_t lds, const void *weight, float eps,
+                                              const void *dS, int64_t ldds, void *dX, int64_t lddx,
+                                              float *dweight, float *dbias, void *workspace, int64_t workspace_bytes,
+                                              gemm_stream_t stream);
+
+/*
+ * Quantisation to 8-bit integers with a scale a row (a token of an
+ * activation, an output channel of a weight stored N x K).  X is M x K, fp32
+ * or bf16.  With amax the largest magnitude of a row:
+ *
+ *     scale = max(amax, 2^-100) / 127          Q = round(x * (127 / max(amax, 2^-100)))
+ *
+ * in fp32, to the nearest integer with ties to even: -127 .. 127.  A row that
+ * holds an infinity or a NaN has codes of 0 and a scale of NaN, so that the
+ * products made of it are NaN.  Row i of Q starts at Q + i*ldq; scales has M
+ * values.
+ */
+GEMM_API gemm_status gemm_quantize_int8(int32_t dtype, int64_t M, int64_t K, const void *X, int64_t ldx,
+                                        int8_t *Q, int64_t ldq, float *scales, gemm_stream_t stream);
+
+/*
+ * Scales of 8-bit integer operands, and the bias; strides in floats, >= 0
+ * (0 shares a value along that direction):
+ *   scale of row i of A                        a[i*a_row]
+ *   scale of group g's column j of the product b[g*b_group + j*b_col]
+ *   bias of group g's column j                 bias[g*bias_group + j]     (NULL: none)
+ */
+typedef struct gemm_int8_scales {
+    const float *a;
+    int64_t a_row;
+    const float *b;
+    int64_t b_col, b_group;
+    const float *bias;
+    int64_t bias_group;
+} gemm_int8_scales;
+
+/*
+ * Product of 8-bit integers with a scale for each row of A (token) and each
+ * column of the product (output channel), dense or grouped by expert:
+ *
+ *     out[i][j] = a(i) * b(g, j) * (sum over k of A[i][k] * B_g[k][j]) + bias(g, j)
+ *
+ * for every row i of group g; groups, ends, stride_b, op_b and the rows past
+ * the last end (zeros) are as in gemm_grouped.  ends NULL: one group of all M
+ * rows (groups must be 1).  A and B hold any 8-bit values, -128 included.
+ * Sums are exact 32-bit integers, which K <= 131071 ensures (GEMM_ERR_UNSUPPORTED
+ * past that); a sum is rounded to fp32 and scaled by b, rounded, and that
+ * times a, plus the bias, is rounded once.  out is fp32 or bf16.  K == 0 gives
+ * the bias, and reads no operand and no scale.
+ */
+GEMM_API gemm_status gemm_int8(int32_t op_b, int32_t groups, const int32_t *ends, int64_t M, int64_t N, int64_t K,
+                               const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, int64_t stride_b,
+                               const gemm_int8_scales *scales, int32_t out_type, void *out, int64_t ldo,
+                               gemm_stream_t stream);
+
+/*
+ * Tokens sorted by expert: the plan.  experts holds `top` choices of each of
+ * `tokens` tokens (row t at experts + t*ld), group numbers of id_bytes 4
+ * (int32_t) or 8 (int64_t) bytes; a number outside 0 .. groups-1 gives its
+ * choice no row (an expert that another GPU holds, a padding token).  Choice
+ * t*top + k is choice k of token t.  The choices that have a row are sorted by
+ * group, those of a group in the order of their numbers:
+ *
+ *     ends[g]           row that group g ends before (groups of them; what gemm_grouped reads)
+ *     place[t*top + k]  row of that choice, or -1
+ *     order[i]          choice of row i, or -1 from the last end on (tokens*top; NULL: not stored)
+ *
+ * tokens*top <= 2^30, 1 <= groups <= 4096 (GEMM_ERR_UNSUPPORTED past that).
+ * `workspace` holds gemm_expert_plan_workspace_size(tokens, top, groups)
+ * bytes, 0 for the smaller calls (4-byte aligned, contents need no clearing;
+ * GEMM_ERR_SCRATCH if it does not).
+ */
+GEMM_API int64_t gemm_expert_plan_workspace_size(int64_t tokens, int32_t top, int32_t groups);
+GEMM_API gemm_status gemm_expert_plan(int32_t id_bytes, int64_t tokens, int32_t top, int32_t groups,
+                                      const void *experts, int64_t ld, int32_t *order, int32_t *place, int32_t *ends,
+                                      void *workspace, int64_t workspace_bytes, gemm_stream_t stream);
+
+/*
+ * Rows handed out to the experts:
+ *
+ *     out[place[t*top + k]] = x[t]
+ *
+ * for values of elem_bytes 1, 2 or 4 bytes, whatever they hold.  X is tokens x
+ * N, out rows x N.  last (NULL: not given) points to the row that the last
+ * group ends before, the plan's ends + groups - 1, read on the device: rows
+ * from there on become zero, others that no place names are left as they
+ * were.  A place outside 0 .. rows-1 (or from *last on) is taken as none;
+ * places must be distinct.  scale_cols > 0 moves as many floats a token
+ * along, from scales (row t at t*lds) to out_scales (row i at i*ldos): the
+ * scales of quantised rows.  out overlaps no input.
+ */
+GEMM_API gemm_status gemm_dispatch(int32_t elem_bytes, int64_t tokens, int32_t top, int64_t N, const void *X,
+                                   int64_t ldx, const int32_t *place, const int32_t *last, int64_t rows, void *out,
+                                   int64_t ldo, int64_t scale_cols, const float *scales, int64_t lds,
+                                   float *out_scales, int64_t ldos, gemm_stream_t stream);
+
+/*
+ * Rows put together again:
+ *
+ *     out[t] = residual[t] + sum over k of weights[t*ldw + k] * rows[place[t*top + k]]
+ *
+ * in the order of k, in fp32, rounded once.  rows is n_rows x N, residual
+ * (NULL: none) and out tokens x N, all of type dtype (fp32 or bf16); weights
+ * are fp32 (NULL: all 1, which makes this the gradient of gemm_dispatch, with
+ * what reaches x another way as residual).  A choice whose place is outside
+ * 0 .. n_rows-1 adds nothing, whatever its weight.  out may be residual itself.
+ */
+GEMM_API gemm_status gemm_combine(int32_t dtype, int64_t tokens, int32_t top, int64_t N, const void *rows,
+                                  int64_t ldr, int64_t n_rows, const int32_t *place, const float *weights,
+                                  int64_t ldw, const void *residual, int64_t ld_res, void *out, int64_t ldo,
+                                  gemm_stream_t stream);
+
+/*
+ * Gradients of gemm_combine (that of the residual is dout itself):
+ *
+ *     drows[place[t*top + k]] = weights[t*ldw + k] * dout[t]
+ *     dweights[t*lddw + k] = sum over columns of dout[t] * rows[place[t*top + k]]     (fp32; 0 without a row)
+ *
+ * dweights may be NULL (not wanted; rows is then not read).  drows is n_rows x
+ * N; last, places and rows that no place names are as in gemm_dispatch.
+ * drows may be rows itself.
+ */
+GEMM_API gemm_status gemm_combine_backward(int32_t dtype, int64_t tokens, int32_t top, int64_t N, const void *dout,
+                                           int64_t lddo, const void *rows, int64_t ldr, int64_t n_rows,
+                                           const int32_t *place, const int32_t *last, const float *weights,
+                                           int64_t ldw, void *drows, int64_t lddr, float *dweights, int64_t lddw,
+                                           gemm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,9 +19,14 @@ from ._lib import (  # noqa: F401  (re-exported C ABI)
     gemm_plan_query, gemm_status_string, gemm_workspace_size, gemm_autotune, gemm_autotune_general, gemm_tuning_count,
     gemm_tuning_clear, gemm_tuning_save, gemm_tuning_load, load, gemm_general_noalloc, GEMM_ERR_SCRATCH,
     GEMM_STATIC_SCRATCH_BYTES, GEMM_SCALE_BLOCK, BlockScales, gemm_quantize, gemm_rms_norm,
-    gemm_rms_norm_workspace_size, gemm_rms_norm_backward, gemm_block_scaled, gemm_grouped, gemm_grouped_wgrad)
+    gemm_rms_norm_workspace_size, gemm_rms_norm_backward, gemm_block_scaled, gemm_grouped, gemm_grouped_wgrad,
+    GEMM_OUT_INT8, Int8Scales, gemm_layer_norm, gemm_layer_norm_workspace_size, gemm_layer_norm_backward,
+    gemm_quantize_int8, gemm_int8, gemm_expert_plan_workspace_size, gemm_expert_plan, gemm_dispatch, gemm_combine,
+    gemm_combine_backward)
 from .experts import (  # noqa: F401
-    block_gemm, grouped_gemm, grouped_wgrad, quantize, rms_norm, rms_norm_backward)
+    block_gemm, grouped_gemm, grouped_wgrad, int8_gemm, layer_norm, layer_norm_backward, quantize, quantize_int8,
+    rms_norm, rms_norm_backward)
+from .routing import combine, combine_backward, dispatch, expert_plan  # noqa: F401
 
 __all__ = ["gemm", "gemm_f32", "gemm_bf16f32", "gemm_f32_ex", "gemm_bf16f32_ex", "gemm_f32_ws", "gemm_bf16f32_ws",
            "gemm_f32_epi", "gemm_bf16f32_epi", "Epilogue", "GEMM_ACT_NONE", "GEMM_ACT_RELU", "GEMM_ACT_GELU",
@@ -34,7 +39,12 @@ __all__ = ["gemm", "gemm_f32", "gemm_bf16f32", "gemm_f32_ex", "gemm_bf16f32_ex",
            "GEMM_ERR_SCRATCH", "GEMM_STATIC_SCRATCH_BYTES", "GEMM_SCALE_BLOCK", "BlockScales",
            "gemm_quantize", "gemm_rms_norm", "gemm_rms_norm_workspace_size", "gemm_rms_norm_backward",
            "gemm_block_scaled", "gemm_grouped", "gemm_grouped_wgrad",
-           "block_gemm", "grouped_gemm", "grouped_wgrad", "quantize", "rms_norm", "rms_norm_backward"]
+           "block_gemm", "grouped_gemm", "grouped_wgrad", "quantize", "rms_norm", "rms_norm_backward",
+           "GEMM_OUT_INT8", "Int8Scales", "gemm_layer_norm", "gemm_layer_norm_workspace_size",
+           "gemm_layer_norm_backward", "gemm_quantize_int8", "gemm_int8", "gemm_expert_plan_workspace_size",
+           "gemm_expert_plan", "gemm_dispatch", "gemm_combine", "gemm_combine_backward",
+           "layer_norm", "layer_norm_backward", "quantize_int8", "int8_gemm", "expert_plan", "dispatch", "combine",
+           "combine_backward"]
 
 
 def _ld(t, what: str) -> int:

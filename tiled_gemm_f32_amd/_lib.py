@@ -43,6 +43,7 @@ GEMM_ACT_GELU = 2
 GEMM_OUT_F32 = 0
 GEMM_OUT_BF16 = 1
 GEMM_OUT_FP8 = 2
+GEMM_OUT_INT8 = 3
 
 # Every entry point include/gemm.h declares.
 EXPORTED = ("gemm_f32", "gemm_bf16f32", "gemm_status_string", "gemm_kernel_count",
@@ -51,7 +52,10 @@ EXPORTED = ("gemm_f32", "gemm_bf16f32", "gemm_status_string", "gemm_kernel_count
             "gemm_tuning_clear", "gemm_tuning_save", "gemm_tuning_load", "gemm_f32_epi", "gemm_bf16f32_epi",
             "gemm_general", "gemm_plan_query_general", "gemm_plan_query_epi", "gemm_autotune_general",
             "gemm_general_noalloc", "gemm_quantize", "gemm_rms_norm", "gemm_rms_norm_workspace_size",
-            "gemm_rms_norm_backward", "gemm_block_scaled", "gemm_grouped", "gemm_grouped_wgrad")
+            "gemm_rms_norm_backward", "gemm_block_scaled", "gemm_grouped", "gemm_grouped_wgrad", "gemm_layer_norm",
+            "gemm_layer_norm_workspace_size", "gemm_layer_norm_backward", "gemm_quantize_int8", "gemm_int8",
+            "gemm_expert_plan_workspace_size", "gemm_expert_plan", "gemm_dispatch", "gemm_combine",
+            "gemm_combine_backward")
 
 # Values along k (and columns of B) that share a block scale.
 GEMM_SCALE_BLOCK = 128
@@ -82,6 +86,13 @@ class BlockScales(ctypes.Structure):
     """gemm_block_scales: device pointers to the scales of A and of B and their strides in floats."""
     _fields_ = [("a", ctypes.c_void_p), ("a_row", ctypes.c_int64), ("a_block", ctypes.c_int64),
                 ("b", ctypes.c_void_p), ("b_n", ctypes.c_int64), ("b_k", ctypes.c_int64), ("b_group", ctypes.c_int64)]
+
+
+class Int8Scales(ctypes.Structure):
+    """gemm_int8_scales: device pointers to the scales of A's rows and of the product's columns and to the
+    bias (0: none), and their strides in floats."""
+    _fields_ = [("a", ctypes.c_void_p), ("a_row", ctypes.c_int64), ("b", ctypes.c_void_p), ("b_col", ctypes.c_int64),
+                ("b_group", ctypes.c_int64), ("bias", ctypes.c_void_p), ("bias_group", ctypes.c_int64)]
 
 
 def _epi(epilogue):
@@ -171,8 +182,25 @@ def load() -> ctypes.CDLL:
     lib.gemm_grouped.argtypes = [i32, i32, i32, vp, i64, i64, i64, f32, vp, i64, vp, i64, i64, scales, i32, vp, i64,
                                  vp]
     lib.gemm_grouped_wgrad.argtypes = [i32, i32, vp, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, i64, vp]
+    lib.gemm_layer_norm.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp, f32, vp, i64, i32, vp, i64, vp, i64, vp]
+    lib.gemm_layer_norm_workspace_size.argtypes = [i64, i64]
+    lib.gemm_layer_norm_workspace_size.restype = i64
+    lib.gemm_layer_norm_backward.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, vp, vp,
+                                             i64, vp]
+    lib.gemm_quantize_int8.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp]
+    lib.gemm_int8.argtypes = [i32, i32, vp, i64, i64, i64, vp, i64, vp, i64, i64, ctypes.POINTER(Int8Scales), i32, vp,
+                              i64, vp]
+    lib.gemm_expert_plan_workspace_size.argtypes = [i64, i32, i32]
+    lib.gemm_expert_plan_workspace_size.restype = i64
+    lib.gemm_expert_plan.argtypes = [i32, i64, i32, i32, vp, i64, vp, vp, vp, vp, i64, vp]
+    lib.gemm_dispatch.argtypes = [i32, i64, i32, i64, vp, i64, vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp]
+    lib.gemm_combine.argtypes = [i32, i64, i32, i64, vp, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_combine_backward.argtypes = [i32, i64, i32, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp, i64,
+                                          vp]
     for fn in (lib.gemm_quantize, lib.gemm_rms_norm, lib.gemm_rms_norm_backward, lib.gemm_block_scaled,
-               lib.gemm_grouped, lib.gemm_grouped_wgrad):
+               lib.gemm_grouped, lib.gemm_grouped_wgrad, lib.gemm_layer_norm, lib.gemm_layer_norm_backward,
+               lib.gemm_quantize_int8, lib.gemm_int8, lib.gemm_expert_plan, lib.gemm_dispatch, lib.gemm_combine,
+               lib.gemm_combine_backward):
         fn.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -347,3 +375,55 @@ def gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, be
                        stream=0) -> int:
     return load().gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w,
                                      stream)
+
+
+def gemm_layer_norm(dtype, M, N, X, ldx, residual, ldr, weight, bias, eps, sum, ld_sum, out_type, out, ldo, scales=0,
+                    ld_scales=0, stream=0) -> int:
+    return load().gemm_layer_norm(dtype, M, N, X, ldx, residual, ldr, weight, bias, eps, sum, ld_sum, out_type, out,
+                                  ldo, scales, ld_scales, stream)
+
+
+def gemm_layer_norm_workspace_size(M, N) -> int:
+    return int(load().gemm_layer_norm_workspace_size(M, N))
+
+
+def gemm_layer_norm_backward(dtype, M, N, dY, lddy, S, lds, weight, eps, dS, ldds, dX, lddx, dweight=0, dbias=0,
+                             workspace=0, workspace_bytes=0, stream=0) -> int:
+    return load().gemm_layer_norm_backward(dtype, M, N, dY, lddy, S, lds, weight, eps, dS, ldds, dX, lddx, dweight,
+                                           dbias, workspace, workspace_bytes, stream)
+
+
+def gemm_quantize_int8(dtype, M, K, X, ldx, Q, ldq, scales, stream=0) -> int:
+    return load().gemm_quantize_int8(dtype, M, K, X, ldx, Q, ldq, scales, stream)
+
+
+def gemm_int8(op_b, groups, ends, M, N, K, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream=0) -> int:
+    return load().gemm_int8(op_b, groups, ends, M, N, K, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream)
+
+
+def gemm_expert_plan_workspace_size(tokens, top, groups) -> int:
+    return int(load().gemm_expert_plan_workspace_size(tokens, top, groups))
+
+
+def gemm_expert_plan(id_bytes, tokens, top, groups, experts, ld, order, place, ends, workspace=0, workspace_bytes=0,
+                     stream=0) -> int:
+    return load().gemm_expert_plan(id_bytes, tokens, top, groups, experts, ld, order, place, ends, workspace,
+                                   workspace_bytes, stream)
+
+
+def gemm_dispatch(elem_bytes, tokens, top, N, X, ldx, place, last, rows, out, ldo, scale_cols=0, scales=0, lds=0,
+                  out_scales=0, ldos=0, stream=0) -> int:
+    return load().gemm_dispatch(elem_bytes, tokens, top, N, X, ldx, place, last, rows, out, ldo, scale_cols, scales,
+                                lds, out_scales, ldos, stream)
+
+
+def gemm_combine(dtype, tokens, top, N, rows, ldr, n_rows, place, weights, ldw, residual, ld_res, out, ldo,
+                 stream=0) -> int:
+    return load().gemm_combine(dtype, tokens, top, N, rows, ldr, n_rows, place, weights, ldw, residual, ld_res, out,
+                               ldo, stream)
+
+
+def gemm_combine_backward(dtype, tokens, top, N, dout, lddo, rows, ldr, n_rows, place, last, weights, ldw, drows, lddr,
+                          dweights=0, lddw=0, stream=0) -> int:
+    return load().gemm_combine_backward(dtype, tokens, top, N, dout, lddo, rows, ldr, n_rows, place, last, weights,
+                                        ldw, drows, lddr, dweights, lddw, stream)

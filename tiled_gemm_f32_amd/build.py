@@ -38,9 +38,10 @@ SOURCES = ["gemm_api.cpp", "gemm_f32_tiled.hip", "gemm_bf16_tiled.hip", "gemm_f3
            "gemm_general.hip", "gemm_bf16_skinny.hip", "gemm_skinny_nt.hip", "gemm_scratch.hip",
            "gemm_bf16_lines.hip", "gemm_fp8_lines.hip", "gemm_fp8_skinny.hip", "gemm_experts_api.cpp",
            "gemm_grouped_general.hip", "gemm_grouped_deep.hip", "gemm_grouped_fp8.hip", "gemm_grouped_bf16.hip",
-           "gemm_grouped_f32.hip", "gemm_grouped_skinny.hip", "gemm_norm.hip"]
+           "gemm_grouped_f32.hip", "gemm_grouped_skinny.hip", "gemm_norm.hip", "gemm_layer_norm.hip", "gemm_route.hip",
+           "gemm_route_api.cpp", "gemm_grouped_int8.hip"]
 HEADERS = ["gemm_device.hpp", "gemm_kernels.hpp", "gemm_lines.hpp", "gemm_grouped.hpp", "gemm_grouped_tile.hpp",
-           "gemm_norm.hpp"]
+           "gemm_norm.hpp", "gemm_rows.hpp", "gemm_route.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

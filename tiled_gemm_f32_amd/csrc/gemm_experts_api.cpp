@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxDim = 0x7fffffff;
 constexpr int64_t kMaxGroups = 65535;          // a grid dimension
+constexpr int64_t kMaxInt8K = 131071;          // products of -128 and -128 that a 32-bit sum holds
 // Workgroups of one launch: their threads along x (512 each at most) are counted in 32 bits.
 constexpr int64_t kMaxTiles = (int64_t(1) << 32) / 512 - 1;
 
@@ -254,6 +255,133 @@ GEMM_API gemm_status gemm_rms_norm_backward(int32_t dtype, int64_t M, int64_t N,
     const gemm::NormGradParams p = {dY, S, weight, dS, dX, dweight, static_cast<float *>(workspace), M, N, lddy, lds,
                                     ldds, lddx, eps, dtype};
     return launched(gemm::launch_rms_norm_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+GEMM_API gemm_status gemm_layer_norm(int32_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx,
+                                     const void *residual, int64_t ldr, const void *weight, const void *bias,
+                                     float eps, void *sum, int64_t ld_sum, int32_t out_type, void *out, int64_t ldo,
+                                     float *scales, int64_t ld_scales, gemm_stream_t stream) {
+    if (!float_type(dtype) || out_type < GEMM_OUT_F32 || out_type > GEMM_OUT_INT8 || M < 0 || N < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return GEMM_ERR_INVALID_ARG;
+    const int64_t row = at_least_1(N);
+    if (ldx < row || ldo < row || (residual != nullptr && ldr < row) || (sum != nullptr && ld_sum < row))
+        return GEMM_ERR_INVALID_ARG;
+    const bool codes = out_type == GEMM_OUT_FP8 || out_type == GEMM_OUT_INT8;
+    const int64_t per_row = out_type == GEMM_OUT_FP8 ? at_least_1(ceil_div(N, GEMM_SCALE_BLOCK)) : 1;
+    if (codes && ld_scales < per_row) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || ldx > kMaxDim || ldo > kMaxDim || (residual != nullptr && ldr > kMaxDim) ||
+        (sum != nullptr && ld_sum > kMaxDim) || (codes && ld_scales > kMaxDim))
+        return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const uintptr_t esz = size_of(dtype);
+    if (bad_ptr(X, esz) || bad_ptr(weight, esz) || bad_opt(bias, esz) || bad_opt(residual, esz) || bad_opt(sum, esz) ||
+        bad_ptr(out, codes ? 1 : out_type == GEMM_OUT_BF16 ? 2 : 4) || (codes && bad_ptr(scales, 4)))
+        return GEMM_ERR_INVALID_ARG;
+    gemm_status st = gemm::check_device();
+    if (st != GEMM_OK) return st;
+    const gemm::LayerNormParams p = {X,   residual, weight, bias, sum,       out, scales, M,       N,
+                                     ldx, ldr,      ld_sum, ldo,  ld_scales, eps, dtype,  out_type};
+    return launched(gemm::launch_layer_norm(p, static_cast<hipStream_t>(stream)));
+}
+
+GEMM_API int64_t gemm_layer_norm_workspace_size(int64_t M, int64_t N) {
+    if (M <= 0 || N <= 0 || M > kMaxDim || N > kMaxDim) return 0;
+    return (int64_t)gemm::layer_norm_grad_partials(M, N) * N * 8;
+}
+
+GEMM_API gemm_status gemm_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, int64_t lddy,
+                                              const void *S, int64_t lds, const void *weight, float eps,
+                                              const void *dS, int64_t ldds, void *dX, int64_t lddx, float *dweight,
+                                              float *dbias, void *workspace, int64_t workspace_bytes,
+                                              gemm_stream_t stream) {
+    if (!float_type(dtype) || M < 0 || N < 0 || workspace_bytes < 0) return GEMM_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return GEMM_ERR_INVALID_ARG;
+    const int64_t row = at_least_1(N);
+    if (lddy < row || lds < row || lddx < row || (dS != nullptr && ldds < row)) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || lddy > kMaxDim || lds > kMaxDim || lddx > kMaxDim ||
+        (dS != nullptr && ldds > kMaxDim))
+        return GEMM_ERR_UNSUPPORTED;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    if (N == 0 || (M == 0 && !sums)) return GEMM_OK;
+    const uintptr_t esz = size_of(dtype);
+    if (bad_opt(dweight, 4) || bad_opt(dbias, 4)) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && (bad_ptr(dY, esz) || bad_ptr(S, esz) || bad_ptr(weight, esz) || bad_ptr(dX, esz) || bad_opt(dS, esz)))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && sums) {
+        if (bad_opt(workspace, 4)) return GEMM_ERR_INVALID_ARG;
+        if (workspace == nullptr || workspace_bytes < gemm_layer_norm_workspace_size(M, N)) return GEMM_ERR_SCRATCH;
+    }
+    gemm_status st = gemm::check_device();
+    if (st != GEMM_OK) return st;
+    const gemm::LayerNormGradParams p = {dY, S, weight, dS, dX, dweight, dbias,
+                                         sums ? static_cast<float *>(workspace) : nullptr, M, N, lddy, lds, ldds, lddx,
+                                         eps, dtype};
+    return launched(gemm::launch_layer_norm_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+GEMM_API gemm_status gemm_quantize_int8(int32_t dtype, int64_t M, int64_t K, const void *X, int64_t ldx, int8_t *Q,
+                                        int64_t ldq, float *scales, gemm_stream_t stream) {
+    if (!float_type(dtype) || M < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (ldx < at_least_1(K) || ldq < at_least_1(K)) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || K > kMaxDim || ldx > kMaxDim || ldq > kMaxDim) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (bad_ptr(X, size_of(dtype)) || bad_ptr(Q, 1) || bad_ptr(scales, 4)) return GEMM_ERR_INVALID_ARG;
+    gemm_status st = gemm::check_device();
+    if (st != GEMM_OK) return st;
+    const gemm::Int8Params p = {X, reinterpret_cast<uint8_t *>(Q), scales, M, K, ldx, ldq, dtype};
+    return launched(gemm::launch_quantize_int8(p, static_cast<hipStream_t>(stream)));
+}
+
+GEMM_API gemm_status gemm_int8(int32_t op_b, int32_t groups, const int32_t *ends, int64_t M, int64_t N, int64_t K,
+                               const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, int64_t stride_b,
+                               const gemm_int8_scales *scales, int32_t out_type, void *out, int64_t ldo,
+                               gemm_stream_t stream) {
+    if (op_b != GEMM_OP_N && op_b != GEMM_OP_T) return GEMM_ERR_INVALID_ARG;
+    if (out_type < GEMM_OUT_F32 || out_type > GEMM_OUT_INT8) return GEMM_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || groups < 0 || (ends == nullptr && groups > 1))
+        return GEMM_ERR_INVALID_ARG;
+    const int64_t b_len = op_b == GEMM_OP_N ? N : K;       // a stored row of B
+    if (lda < at_least_1(K) || ldb < at_least_1(b_len) || ldo < at_least_1(N) || stride_b < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (scales == nullptr || scales->a_row < 0 || scales->b_col < 0 || scales->b_group < 0 || scales->bias_group < 0)
+        return GEMM_ERR_INVALID_ARG;
+    const bool writes = M > 0 && N > 0, reads = writes && K > 0 && groups > 0;
+    if (reads && (bad_ptr(A, 1) || bad_ptr(B, 1) || bad_ptr(scales->a, 4) || bad_ptr(scales->b, 4)))
+        return GEMM_ERR_INVALID_ARG;
+    if (writes && (bad_ptr(out, out_type == GEMM_OUT_F32 ? 4 : 2) || bad_opt(scales->bias, 4) || bad_opt(ends, 4)))
+        return GEMM_ERR_INVALID_ARG;
+    if (out_type != GEMM_OUT_F32 && out_type != GEMM_OUT_BF16) return GEMM_ERR_UNSUPPORTED;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxInt8K || lda > kMaxDim || ldb > kMaxDim || ldo > kMaxDim ||
+        groups > kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (!writes) return GEMM_OK;
+    if (gemm::most_row_tiles(M, groups, 64, ends != nullptr) * ceil_div(N, 64) > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+    gemm_status st = gemm::check_device();
+    if (st != GEMM_OK) return st;
+    gemm::GroupedParams p = {};
+    p.A = A;
+    p.B = B;
+    p.out = out;
+    p.ends = ends;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.K = (int32_t)K;
+    p.groups = groups;
+    p.lda = lda;
+    p.ldb = ldb;
+    p.stride_b = stride_b;
+    p.ldo = ldo;
+    p.alpha = 1.0f;
+    p.out_type = out_type;
+    p.ts = *scales;
+    if (groups == 0) {                         // all rows are past the last end
+        p.ends = nullptr;
+        p.groups = 1;
+        p.K = 0;
+        p.ts.bias = nullptr;
+    }
+    return launched(gemm::launch_int8_general(op_b, p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -13,6 +13,9 @@
 
 namespace gemm {
 
+// Type of an operand of 8-bit integers, which only gemm_int8 takes, beside those of gemm_dtype.
+constexpr int32_t kInt8 = 16;
+
 // One launch, already validated (gemm_experts_api.cpp): sizes below 2^31,
 // pointers aligned to their elements.
 struct GroupedParams {
@@ -26,6 +29,7 @@ struct GroupedParams {
     float alpha, beta;         // beta: weight gradients only
     int32_t out_type;          // GEMM_OUT_F32 or GEMM_OUT_BF16
     gemm_block_scales sc;      // fp8 only
+    gemm_int8_scales ts;       // 8-bit integers only
     bool by_size;              // weight gradients of at most 64 groups: in the order of their rows
 };
 
@@ -194,6 +198,12 @@ __device__ __forceinline__ int find_group(const GroupedParams &p, int turn, int 
     return g;
 }
 
+// Result of a sum of 8-bit integer products: rounded to fp32 and scaled by the column's scale, rounded; then
+// scaled by the row's and the bias added, rounded once.
+__device__ __forceinline__ float int8_value(int sum, float a, float b, float bias) {
+    return fmaf((float)sum * b, a, bias);
+}
+
 #endif  // __HIPCC__
 
 // Launchers.  The general ones run every type, layout and alignment; the
@@ -215,6 +225,7 @@ hipError_t launch_grouped_deep(int32_t dtype, int32_t op_b, bool dma, const Grou
 hipError_t launch_wgrad_bf16(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_f32(bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_general(int32_t dtype, int32_t op_b, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_int8_general(int32_t op_b, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_wgrad_general(int32_t dtype, const GroupedParams &p, hipStream_t stream);
 
 }  // namespace gemm

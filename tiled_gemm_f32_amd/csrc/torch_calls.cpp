@@ -1,4 +1,4 @@
-// The torch wrappers' common calls (experts.py), checked, allocated and
+// The torch wrappers' common calls (experts.py, routing.py), checked, allocated and
 // forwarded here: in Python that costs the host 9 to 12 us a call, as long as
 // a small kernel runs; here 5 to 7.
 //
@@ -90,6 +90,10 @@ int64_t on16(int64_t n) { return (n + 15) / 16 * 16; }
 
 PyObject *none() { Py_RETURN_NONE; }
 PyObject *give(gemm_status st, const Tensor &a) { return st == GEMM_OK ? THPVariable_Wrap(a) : PyLong_FromLong(st); }
+PyObject *give(gemm_status st, const Tensor &a, const Tensor &b, const Tensor &c) {
+    return st == GEMM_OK ? Py_BuildValue("NNN", THPVariable_Wrap(a), THPVariable_Wrap(b), THPVariable_Wrap(c))
+                         : PyLong_FromLong(st);
+}
 PyObject *give(gemm_status st, const Tensor &a, const Tensor &b) {
     return st == GEMM_OK ? Py_BuildValue("NN", THPVariable_Wrap(a), THPVariable_Wrap(b)) : PyLong_FromLong(st);
 }
@@ -285,9 +289,266 @@ PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+Tensor row_of(const Tensor &like, int64_t n, at::ScalarType type) {
+    return at::empty_strided({n}, {1}, like.options().dtype(type));
+}
+
+// layer_norm(x, weight, bias, residual, eps, out_dtype, device, stream)
+PyObject *layer_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix x, r;
+    void *weight, *bias = nullptr;
+    at::ScalarType type, out;
+    int32_t dtype, kind;
+    if (!where(args, n, 8, w) || !float_type(args[0], type, dtype) || !matrix(args[0], w, type, x) ||
+        !vector(args[1], w, type, x.cols, weight) || (args[2] != Py_None && !vector(args[2], w, type, x.cols, bias)) ||
+        !PyFloat_Check(args[4]))
+        return none();
+    if (THPDtype_Check(args[5]) && reinterpret_cast<THPDtype *>(args[5])->scalar_type == at::kChar) {
+        out = at::kChar;
+        kind = GEMM_OUT_INT8;
+    } else if (!out_type(args[5], type, out, kind)) {
+        return none();
+    }
+    const bool with = args[3] != Py_None;
+    if (with && (!matrix(args[3], w, type, r) || r.rows != x.rows || r.cols != x.cols)) return none();
+    const bool fp8 = kind == GEMM_OUT_FP8, int8 = kind == GEMM_OUT_INT8;
+    Tensor sum, scales;
+    if (with) sum = make(*x.t, x.rows, x.cols, x.cols, type);
+    const int64_t ldo = fp8 || int8 ? on16(x.cols) : x.cols, lds = fp8 ? blocks(x.cols) : 1;
+    const Tensor y = make(*x.t, x.rows, x.cols, ldo, out);
+    if (fp8) scales = make(*x.t, x.rows, lds, lds, at::kFloat);
+    if (int8) scales = row_of(*x.t, x.rows, at::kFloat);
+    const gemm_status st = gemm_layer_norm(
+        dtype, x.rows, x.cols, x.data, x.ld, with ? r.data : nullptr, r.ld, weight, bias,
+        (float)PyFloat_AS_DOUBLE(args[4]), with ? sum.data_ptr() : nullptr, with ? x.cols : 0, kind, y.data_ptr(), ldo,
+        fp8 || int8 ? static_cast<float *>(scales.data_ptr()) : nullptr, lds, w.stream);
+    if (st != GEMM_OK) return PyLong_FromLong(st);
+    PyObject *total = with ? THPVariable_Wrap(sum) : Py_NewRef(args[0]);
+    return Py_BuildValue("NNN", THPVariable_Wrap(y), total, fp8 || int8 ? THPVariable_Wrap(scales) : none());
+    END_HANDLE_TH_ERRORS
+}
+
+// layer_norm_backward(dy, summed, weight, dsum, eps, device, stream)
+PyObject *layer_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix dy, s, ds;
+    void *weight;
+    at::ScalarType type;
+    int32_t dtype;
+    if (!where(args, n, 7, w) || !float_type(args[0], type, dtype) || !matrix(args[0], w, type, dy) ||
+        !matrix(args[1], w, type, s) || s.rows != dy.rows || s.cols != dy.cols ||
+        !vector(args[2], w, type, dy.cols, weight) || !PyFloat_Check(args[4]))
+        return none();
+    const bool with = args[3] != Py_None;
+    if (with && (!matrix(args[3], w, type, ds) || ds.rows != dy.rows || ds.cols != dy.cols)) return none();
+    const Tensor dx = make(*dy.t, dy.rows, dy.cols, dy.cols, type);
+    const Tensor dweight = row_of(*dy.t, dy.cols, at::kFloat), dbias = row_of(*dy.t, dy.cols, at::kFloat);
+    const int64_t need = gemm_layer_norm_workspace_size(dy.rows, dy.cols);
+    const Tensor space = row_of(*dy.t, need, at::kByte);
+    return give(gemm_layer_norm_backward(dtype, dy.rows, dy.cols, dy.data, dy.ld, s.data, s.ld, weight,
+                                         (float)PyFloat_AS_DOUBLE(args[4]), with ? ds.data : nullptr, ds.ld,
+                                         dx.data_ptr(), dy.cols, static_cast<float *>(dweight.data_ptr()),
+                                         static_cast<float *>(dbias.data_ptr()), space.data_ptr(), need, w.stream),
+                dx, dweight, dbias);
+    END_HANDLE_TH_ERRORS
+}
+
+// quantize_int8(x, device, stream)
+PyObject *quantize_int8(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix x;
+    at::ScalarType type;
+    int32_t dtype;
+    if (!where(args, n, 3, w) || !float_type(args[0], type, dtype) || !matrix(args[0], w, type, x)) return none();
+    const Tensor codes = make(*x.t, x.rows, x.cols, on16(x.cols), at::kChar);
+    const Tensor scales = row_of(*x.t, x.rows, at::kFloat);
+    return give(gemm_quantize_int8(dtype, x.rows, x.cols, x.data, x.ld, static_cast<int8_t *>(codes.data_ptr()),
+                                   on16(x.cols), static_cast<float *>(scales.data_ptr()), w.stream),
+                codes, scales);
+    END_HANDLE_TH_ERRORS
+}
+
+// A value a column of the product, for each group: [groups,] n floats.
+bool columns(PyObject *o, const Where &w, int dim, int64_t groups, int64_t n, const float *&data, int64_t &col,
+             int64_t &group) {
+    const Tensor *t = tensor(o);
+    if (t == nullptr || t->scalar_type() != at::kFloat || t->dim() != dim || !on(*t, w) || t->size(dim - 1) != n ||
+        (dim == 2 && t->size(0) != groups))
+        return false;
+    data = static_cast<const float *>(t->data_ptr());
+    col = t->stride(dim - 1);
+    group = dim == 2 && groups > 1 ? t->stride(0) : 0;
+    return true;
+}
+
+// int8_gemm(A, B, a_scales, b_scales, ends, bias, op_b, out_dtype, device, stream)
+PyObject *int8_gemm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix A, B;
+    bool t;
+    void *ends = nullptr;
+    at::ScalarType out;
+    int32_t kind;
+    gemm_int8_scales sc = {};
+    int64_t group;
+    if (!where(args, n, 10, w)) return none();
+    const bool grouped = args[4] != Py_None;
+    if (!matrix(args[0], w, at::kChar, A) || !matrix(args[1], w, at::kChar, B, grouped ? 3 : 2) ||
+        (grouped && !vector(args[4], w, at::kInt, B.groups, ends)) || !transposes(args[6], t) ||
+        !out_type(args[7], at::kBFloat16, out, kind) || kind == GEMM_OUT_FP8 || (t ? B.cols : B.rows) != A.cols)
+        return none();
+    const int64_t N = t ? B.rows : B.cols;
+    const int dim = grouped ? 2 : 1;
+    if (!columns(args[2], w, 1, 1, A.rows, sc.a, sc.a_row, group) ||
+        !columns(args[3], w, dim, B.groups, N, sc.b, sc.b_col, sc.b_group))
+        return none();
+    if (args[5] != Py_None) {
+        int64_t col;
+        if (!columns(args[5], w, dim, B.groups, N, sc.bias, col, sc.bias_group) || (N > 1 && col != 1)) return none();
+    }
+    const Tensor y = make(*A.t, A.rows, N, N, out);
+    return give(gemm_int8(t ? GEMM_OP_T : GEMM_OP_N, (int32_t)B.groups, static_cast<const int32_t *>(ends), A.rows, N,
+                          A.cols, static_cast<const int8_t *>(A.data), A.ld, static_cast<const int8_t *>(B.data), B.ld,
+                          B.stride, &sc, kind, y.data_ptr(), N, w.stream),
+                y);
+    END_HANDLE_TH_ERRORS
+}
+
+// expert_plan(experts, groups, device, stream)
+PyObject *expert_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix e;
+    if (!where(args, n, 4, w) || tensor(args[0]) == nullptr || !PyLong_CheckExact(args[1])) return none();
+    const at::ScalarType type = tensor(args[0])->scalar_type();
+    const int64_t groups = PyLong_AsLongLong(args[1]);
+    if (PyErr_Occurred() != nullptr) {
+        PyErr_Clear();
+        return none();
+    }
+    if ((type != at::kInt && type != at::kLong) || !matrix(args[0], w, type, e) || groups < 1 || groups > 1 << 30 ||
+        e.cols > 1 << 30 || e.rows > 1 << 30)
+        return none();
+    const Tensor order = row_of(*e.t, e.rows * e.cols, at::kInt), ends = row_of(*e.t, groups, at::kInt);
+    const Tensor place = make(*e.t, e.rows, e.cols, e.cols, at::kInt);
+    const int64_t need = gemm_expert_plan_workspace_size(e.rows, (int32_t)e.cols, (int32_t)groups);
+    Tensor space;
+    if (need > 0) space = row_of(*e.t, need, at::kByte);
+    return give(gemm_expert_plan(type == at::kLong ? 8 : 4, e.rows, (int32_t)e.cols, (int32_t)groups, e.data, e.ld,
+                                 static_cast<int32_t *>(order.data_ptr()), static_cast<int32_t *>(place.data_ptr()),
+                                 static_cast<int32_t *>(ends.data_ptr()), need > 0 ? space.data_ptr() : nullptr, need,
+                                 w.stream),
+                order, place, ends);
+    END_HANDLE_TH_ERRORS
+}
+
+// A plan's places, tokens x top without padding, and (o not null) its last end.
+bool places(PyObject *o, const Where &w, int64_t tokens, Matrix &place) {
+    return matrix(o, w, at::kInt, place) && place.rows == tokens && place.ld == place.cols && place.cols <= 1 << 30;
+}
+bool last_end(PyObject *o, const Where &w, const int32_t *&last) {
+    const Tensor *t = tensor(o);
+    void *ends;
+    if (t == nullptr || t->dim() != 1 || t->size(0) < 1 || !vector(o, w, at::kInt, t->size(0), ends)) return false;
+    last = static_cast<const int32_t *>(ends) + t->size(0) - 1;
+    return true;
+}
+bool weights_of(PyObject *o, const Where &w, const Matrix &place, Matrix &m) {
+    return matrix(o, w, at::kFloat, m) && m.rows == place.rows && m.cols == place.cols;
+}
+
+// dispatch(x, place, ends, scales, device, stream)
+PyObject *dispatch(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix x, place, sc;
+    const int32_t *last;
+    if (!where(args, n, 6, w) || tensor(args[0]) == nullptr) return none();
+    const at::ScalarType type = tensor(args[0])->scalar_type();
+    if ((type != at::kFloat && type != at::kBFloat16 && type != at::kFloat8_e4m3fn && type != at::kChar) ||
+        !matrix(args[0], w, type, x) || !places(args[1], w, x.rows, place) || !last_end(args[2], w, last))
+        return none();
+    const int64_t rows = place.rows * place.cols;
+    const bool with = args[3] != Py_None;
+    Tensor out_scales;
+    if (with) {
+        const Tensor *t = tensor(args[3]);
+        if (t == nullptr) return none();
+        if (t->dim() == 1) {
+            void *data;
+            if (!vector(args[3], w, at::kFloat, x.rows, data)) return none();
+            sc.data = data;
+            sc.cols = sc.ld = 1;
+            out_scales = row_of(*x.t, rows, at::kFloat);
+        } else {
+            if (!matrix(args[3], w, at::kFloat, sc) || sc.rows != x.rows) return none();
+            out_scales = make(*x.t, rows, sc.cols, sc.cols, at::kFloat);
+        }
+    }
+    const int64_t bytes = (int64_t)x.t->element_size(), ldo = bytes == 1 ? on16(x.cols) : x.cols;
+    const Tensor out = make(*x.t, rows, x.cols, ldo, type);
+    const gemm_status st = gemm_dispatch(
+        (int32_t)bytes, x.rows, (int32_t)place.cols, x.cols, x.data, x.ld, static_cast<const int32_t *>(place.data), last,
+        rows, out.data_ptr(), ldo, sc.cols, static_cast<const float *>(sc.data), sc.ld,
+        with ? static_cast<float *>(out_scales.data_ptr()) : nullptr, sc.cols, w.stream);
+    return with ? give(st, out, out_scales) : give(st, out);
+    END_HANDLE_TH_ERRORS
+}
+
+// combine(rows, place, weights, residual, device, stream)
+PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix rows, place, share, r;
+    at::ScalarType type;
+    int32_t dtype;
+    if (!where(args, n, 6, w) || !float_type(args[0], type, dtype) || !matrix(args[0], w, type, rows) ||
+        tensor(args[1]) == nullptr || tensor(args[1])->dim() != 2 ||
+        !places(args[1], w, tensor(args[1])->size(0), place))
+        return none();
+    if (args[2] != Py_None && !weights_of(args[2], w, place, share)) return none();
+    if (args[3] != Py_None && (!matrix(args[3], w, type, r) || r.rows != place.rows || r.cols != rows.cols))
+        return none();
+    const Tensor out = make(*rows.t, place.rows, rows.cols, rows.cols, type);
+    return give(gemm_combine(dtype, place.rows, (int32_t)place.cols, rows.cols, rows.data, rows.ld, rows.rows,
+                             static_cast<const int32_t *>(place.data), static_cast<const float *>(share.data), share.ld,
+                             r.data, r.ld, out.data_ptr(), rows.cols, w.stream),
+                out);
+    END_HANDLE_TH_ERRORS
+}
+
+// combine_backward(dout, rows, place, weights, ends, device, stream)
+PyObject *combine_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Where w;
+    Matrix d, rows, place, share;
+    const int32_t *last;
+    at::ScalarType type;
+    int32_t dtype;
+    if (!where(args, n, 7, w) || !float_type(args[0], type, dtype) || !matrix(args[0], w, type, d) ||
+        !matrix(args[1], w, type, rows) || rows.cols != d.cols || !places(args[2], w, d.rows, place) ||
+        !weights_of(args[3], w, place, share) || !last_end(args[4], w, last))
+        return none();
+    const Tensor drows = make(*d.t, rows.rows, rows.cols, rows.cols, type);
+    const Tensor dweights = make(*d.t, place.rows, place.cols, place.cols, at::kFloat);
+    return give(gemm_combine_backward(dtype, d.rows, (int32_t)place.cols, d.cols, d.data, d.ld, rows.data, rows.ld,
+                                      rows.rows, static_cast<const int32_t *>(place.data), last,
+                                      static_cast<const float *>(share.data), share.ld, drows.data_ptr(), rows.cols,
+                                      static_cast<float *>(dweights.data_ptr()), place.cols, w.stream),
+                drows, dweights);
+    END_HANDLE_TH_ERRORS
+}
+
 #define CALL(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(quantize), CALL(rms_norm), CALL(rms_norm_backward), CALL(block_gemm),
-                         CALL(grouped_gemm), CALL(grouped_wgrad), {nullptr, nullptr, 0, nullptr}};
+                         CALL(grouped_gemm), CALL(grouped_wgrad), CALL(layer_norm), CALL(layer_norm_backward),
+                         CALL(quantize_int8), CALL(int8_gemm), CALL(expert_plan), CALL(dispatch), CALL(combine),
+                         CALL(combine_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods};
 
 }  // namespace

@@ -1,7 +1,9 @@
 """The operators of a sparse expert layer over torch tensors: block
-quantisation to fp8, RMS norm with the residual's addition (and its
-gradients), the fp8 product with a scale for each block of 128, and products
-grouped by expert (and their weight gradients).
+quantisation to fp8, RMS norm and layer norm with the residual's addition
+(and their gradients), the fp8 product with a scale for each block of 128,
+the product of 8-bit integers with a scale for each token and channel, and
+products grouped by expert (and their weight gradients).  How rows get to the
+experts and back is in routing.py.
 
 Like ``gemm``, these only read shapes, strides and pointers, allocate what
 is not passed in, and forward to the C entry points of include/gemm.h, which
@@ -18,8 +20,9 @@ from __future__ import annotations
 
 from ._lib import (
     GEMM_DTYPE_BF16F32, GEMM_DTYPE_F32, GEMM_DTYPE_FP8F32, GEMM_OK, GEMM_OP_N, GEMM_OP_T, GEMM_OUT_BF16, GEMM_OUT_F32,
-    GEMM_OUT_FP8, GEMM_SCALE_BLOCK, BlockScales, GemmError, gemm_block_scaled, gemm_grouped, gemm_grouped_wgrad,
-    gemm_quantize, gemm_rms_norm, gemm_rms_norm_backward, gemm_rms_norm_workspace_size)
+    GEMM_OUT_FP8, GEMM_OUT_INT8, GEMM_SCALE_BLOCK, BlockScales, GemmError, Int8Scales, gemm_block_scaled, gemm_grouped,
+    gemm_grouped_wgrad, gemm_int8, gemm_layer_norm, gemm_layer_norm_backward, gemm_layer_norm_workspace_size,
+    gemm_quantize, gemm_quantize_int8, gemm_rms_norm, gemm_rms_norm_backward, gemm_rms_norm_workspace_size)
 
 
 # A call costs the host about as long as a small kernel runs.  The common ones
@@ -297,6 +300,153 @@ def rms_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-6, dx=None,
     return dx, dweight
 
 
+def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, out_dtype=None, out=None, summed=None,
+               scales=None, stream=None):
+    """(out, summed, scales) of a row-wise layer norm of ``x`` (+ ``residual``).
+
+    Arguments and results are those of ``rms_norm``, with a ``bias`` (one value
+    a column, of x's type).  ``out`` may also be int8: whole numbers with one
+    scale a row, as ``quantize_int8`` gives them."""
+    import torch
+    if out is None and summed is None and scales is None and stream is None and x.is_cuda:
+        got = _common("layer_norm", x, weight, bias, residual, eps, out_dtype)
+        if got is not None:
+            return got
+    if stream is not None:
+        got = _elsewhere(stream, x, layer_norm, x, weight, bias, residual, eps, out_dtype, out, summed, scales)
+        if got is not None:
+            return got
+    dt = _float_type(x, "x")
+    device = _device(x, "x")
+    _check(x, "x", device)
+    M, N = x.shape
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is None and what == "bias":
+            continue
+        _check(t, what, device, (N,), x.dtype)
+        if N > 1 and t.stride(0) != 1:
+            raise ValueError(f"{what} must be contiguous")
+    r_ptr = s_ptr = c_ptr = ldr = ld_sum = ld_scales = 0
+    if residual is not None:
+        _check(residual, "residual", device, (M, N), x.dtype)
+        r_ptr, ldr = residual.data_ptr(), _ld(residual, "residual")
+    if summed is not None:
+        _check(summed, "summed", device, (M, N), x.dtype)
+        s_ptr, ld_sum = summed.data_ptr(), _ld(summed, "summed")
+    elif residual is not None:
+        summed, ld_sum = _new(M, N, x.dtype, x.device)
+        s_ptr = summed.data_ptr()
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    dtype = out.dtype if out is not None else out_dtype or x.dtype
+    kind = GEMM_OUT_INT8 if dtype is torch.int8 else _out_type(dtype, "out")
+    codes = kind in (GEMM_OUT_FP8, GEMM_OUT_INT8)
+    if out is not None:
+        _check(out, "out", device, (M, N))
+        ldo = _ld(out, "out")
+    else:
+        out, ldo = _new(M, N, dtype, x.device, 16 if codes else 1)
+    if codes:
+        shape = (M, _blocks(N)) if kind == GEMM_OUT_FP8 else (M,)
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        _check(scales, "scales", device, shape, torch.float32)
+        if kind == GEMM_OUT_FP8:
+            ld_scales = _ld(scales, "scales")
+        else:
+            ld_scales = scales.stride(0) if M > 1 else 1
+            if ld_scales < 1:
+                raise ValueError("scales must not overlap")
+        c_ptr = scales.data_ptr()
+    elif scales is not None:
+        raise ValueError("scales go with a float8_e4m3fn or int8 output")
+    _call("layer_norm", device, gemm_layer_norm, dt, M, N, x.data_ptr(), _ld(x, "x"), r_ptr, ldr, weight.data_ptr(),
+          bias.data_ptr() if bias is not None else 0, float(eps), s_ptr, ld_sum, kind, out.data_ptr(), ldo, c_ptr,
+          ld_scales)
+    return out, summed if summed is not None else x, scales
+
+
+def layer_norm_backward(dy, summed, weight, dsum=None, eps: float = 1e-5, dx=None, want_dweight: bool = True,
+                        want_dbias: bool = True, stream=None):
+    """(dx, dweight, dbias) of ``layer_norm``, from the gradient ``dy`` of its output.
+
+    ``summed`` is what the forward pass returned; ``dsum`` the gradient that
+    reaches it past the norm.  dx is the gradient of x and of the residual
+    alike (it may be passed as dy or dsum); dweight and dbias are float32, or
+    None where they are not wanted."""
+    import torch
+    if dx is None and want_dweight and want_dbias and stream is None and dy.is_cuda:
+        got = _common("layer_norm_backward", dy, summed, weight, dsum, eps)
+        if got is not None:
+            return got
+    if stream is not None:
+        got = _elsewhere(stream, dy, layer_norm_backward, dy, summed, weight, dsum, eps, dx, want_dweight, want_dbias)
+        if got is not None:
+            return got
+    dt = _float_type(dy, "dy")
+    device = _device(dy, "dy")
+    _check(dy, "dy", device)
+    M, N = dy.shape
+    _check(summed, "summed", device, (M, N), dy.dtype)
+    _check(weight, "weight", device, (N,), dy.dtype)
+    if N > 1 and weight.stride(0) != 1:
+        raise ValueError("weight must be contiguous")
+    if dsum is not None:
+        _check(dsum, "dsum", device, (M, N), dy.dtype)
+    if dx is None:
+        dx, lddx = _new(M, N, dy.dtype, dy.device)
+    else:
+        _check(dx, "dx", device, (M, N), dy.dtype)
+        lddx = _ld(dx, "dx")
+    dweight = torch.empty(N, dtype=torch.float32, device=dy.device) if want_dweight else None
+    dbias = torch.empty(N, dtype=torch.float32, device=dy.device) if want_dbias else None
+    ws_ptr = need = 0
+    if want_dweight or want_dbias:
+        need = gemm_layer_norm_workspace_size(M, N)
+        ws = torch.empty(max(need, 4), dtype=torch.uint8, device=dy.device)
+        ws_ptr = ws.data_ptr()
+    _call("layer_norm_backward", device, gemm_layer_norm_backward, dt, M, N, dy.data_ptr(), _ld(dy, "dy"),
+          summed.data_ptr(), _ld(summed, "summed"), weight.data_ptr(), float(eps),
+          dsum.data_ptr() if dsum is not None else 0, _ld(dsum, "dsum") if dsum is not None else 0, dx.data_ptr(), lddx,
+          dweight.data_ptr() if want_dweight else 0, dbias.data_ptr() if want_dbias else 0, ws_ptr, need)
+    return dx, dweight, dbias
+
+
+def quantize_int8(x, out=None, scales=None, stream=None):
+    """(codes, scales) of a float32 or bfloat16 matrix in int8, a scale a row.
+
+    ``x`` is about ``codes * scales[:, None]``: rows are tokens of an activation,
+    or output channels of a weight stored N x K.  A row that holds an infinity
+    or a NaN gets a scale of NaN.  Codes allocated here have rows padded to 16
+    bytes."""
+    import torch
+    if out is None and scales is None and stream is None and x.is_cuda:
+        got = _common("quantize_int8", x)
+        if got is not None:
+            return got
+    if stream is not None:
+        got = _elsewhere(stream, x, quantize_int8, x, out, scales)
+        if got is not None:
+            return got
+    dt = _float_type(x, "x")
+    device = _device(x, "x")
+    _check(x, "x", device)
+    M, K = x.shape
+    if out is None:
+        out, ldq = _new(M, K, torch.int8, x.device, 16)
+    else:
+        _check(out, "out", device, (M, K), torch.int8)
+        ldq = _ld(out, "out")
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check(scales, "scales", device, (M,), torch.float32)
+    if M > 1 and scales.stride(0) != 1:
+        raise ValueError("scales must be contiguous")
+    _call("quantize_int8", device, gemm_quantize_int8, dt, M, K, x.data_ptr(), _ld(x, "x"), out.data_ptr(), ldq,
+          scales.data_ptr())
+    return out, scales
+
+
 def _strides(scales, lead: int, shape, what: str):
     """Strides of a scale tensor's last two dimensions, after checking its shape."""
     if scales.shape != shape:
@@ -456,4 +606,51 @@ def grouped_wgrad(dy, x, ends, alpha: float = 1.0, beta: float = 0.0, out=None, 
     _call("grouped_wgrad", device, gemm_grouped_wgrad, dt, groups, ends.data_ptr(), M, N, K,
           float(alpha), dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), float(beta), out.data_ptr(),
           _ld(out, "out"), out.stride(0) if groups > 1 else 0)
+    return out
+
+
+def int8_gemm(A, B, a_scales, b_scales, ends=None, bias=None, op_b: str = "T", out=None, out_dtype=None, stream=None):
+    """out[i, j] = a_scales[i] * b_scales[j] * (A @ op(B))[i, j] + bias[j] of int8 operands.
+
+    A is M x K with a scale a row.  ``op_b`` "T": B is N x K, "N": K x N;
+    b_scales and the bias (float32) have a value a column of the product.  With
+    ``ends``, A's rows are sorted by group as in ``grouped_gemm``, B is groups x
+    N x K (or K x N), b_scales and bias are groups x N, and rows past the last
+    end become zero.  The products are summed exactly (K is at most 131071).
+    ``out`` is bfloat16 by default, or float32."""
+    import torch
+    if out is None and stream is None and A.is_cuda:
+        got = _common("int8_gemm", A, B, a_scales, b_scales, ends, bias, op_b, out_dtype)
+        if got is not None:
+            return got
+    if stream is not None:
+        got = _elsewhere(stream, A, int8_gemm, A, B, a_scales, b_scales, ends, bias, op_b, out, out_dtype)
+        if got is not None:
+            return got
+    if op_b not in ("N", "T"):
+        raise ValueError("op_b is 'N' or 'T'")
+    device = _device(A, "A")
+    _check(A, "A", device, dtype=torch.int8)
+    _check(B, "B", device, dtype=torch.int8, dim=2 if ends is None else 3)
+    M, K = A.shape
+    N, K2 = B.shape[-2:] if op_b == "T" else (B.shape[-1], B.shape[-2])
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, op_b={op_b} {tuple(B.shape)}")
+    groups, shape = (1, (N,)) if ends is None else (B.shape[0], (B.shape[0], N))
+    if ends is not None:
+        _check_ends(ends, device, groups)
+    _check(a_scales, "a_scales", device, (M,), torch.float32)
+    _check(b_scales, "b_scales", device, shape, torch.float32)
+    if bias is not None:
+        _check(bias, "bias", device, shape, torch.float32)
+        if N > 1 and bias.stride(-1) != 1:
+            raise ValueError("bias must have unit stride along its columns")
+    apart = groups > 1
+    sc = Int8Scales(a_scales.data_ptr(), a_scales.stride(0), b_scales.data_ptr(), b_scales.stride(-1),
+                    b_scales.stride(0) if apart else 0, bias.data_ptr() if bias is not None else 0,
+                    bias.stride(0) if apart and bias is not None else 0)
+    out, ldo, kind = _product_out(M, N, out, out_dtype, torch.bfloat16, A, device)
+    _call("int8_gemm", device, gemm_int8, GEMM_OP_T if op_b == "T" else GEMM_OP_N, groups,
+          ends.data_ptr() if ends is not None else 0, M, N, K, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
+          B.stride(0) if apart else 0, sc, kind, out.data_ptr(), ldo)
     return out
