@@ -200,8 +200,8 @@ __device__ __forceinline__ int find_group(const GroupedParams &p, int turn, int 
 
 // Result of a sum of 8-bit integer products: rounded to fp32 and scaled by the column's scale, rounded; then
 // scaled by the row's and the bias added, rounded once.
-__device__ __forceinline__ float int8_value(int sum, float a, float b, float bias) {
-    return fmaf((float)sum * b, a, bias);
+__device__ __forceinline__ float int8_value(float sum, float a, float b, float bias) {
+    return fmaf(sum * b, a, bias);
 }
 
 #endif  // __HIPCC__
@@ -210,6 +210,7 @@ __device__ __forceinline__ float int8_value(int sum, float a, float b, float bia
 // others the tiles of gemm_grouped_tile.hpp.  dma: rows of both operands
 // start on 16 bytes.
 hipError_t launch_grouped_fp8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
+hipError_t launch_grouped_int8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_bf16(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 hipError_t launch_grouped_f32(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);
 // Few rows (on average 64 a group at most) and weights stored N x K, rows on
@@ -218,7 +219,7 @@ int skinny_rows(int32_t dtype, int32_t op_b, const GroupedParams &p);
 hipError_t launch_grouped_skinny(int32_t dtype, int rows, const GroupedParams &p, hipStream_t stream);
 // Few output tiles: whether the kernel whose waves share out k can run the call, and that kernel.
 constexpr int deep_columns(int32_t dtype, bool kn) {         // of its tiles of 32 rows
-    return !kn || dtype == GEMM_DTYPE_F32 ? 32 : dtype == GEMM_DTYPE_BF16F32 ? 64 : 128;
+    return !kn || dtype == GEMM_DTYPE_F32 ? 32 : dtype == GEMM_DTYPE_BF16F32 ? 64 : 128;      // (bytes: 128)
 }
 bool deep_takes(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p);
 hipError_t launch_grouped_deep(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream);

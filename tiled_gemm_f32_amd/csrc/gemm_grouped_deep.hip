@@ -84,7 +84,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     };
 
     const int slabs = slabs_of(len, C::BK);
-    f32x16 acc[FN] = {};
+    typename C::Acc acc[FN] = {};
     // This wave's slabs: wave, wave + WAVES, ...
     const int mine = (slabs - wave + WAVES - 1) / WAVES;
     if (mine > 0) fetch(wave);
@@ -136,29 +136,43 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     if (mine > 0) step(mine - 1, true);
 
     // Partial tiles: row l32 of 8 * FN chunks of 4 columns, chunk c at c ^ (row & 7).
+    typedef std::conditional_t<C::I8, int, float> Sum;
+    typedef std::conditional_t<C::I8, i32x4, f32x4> Sums;
     float *const tile = reinterpret_cast<float *>(st);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<f32x4 *>(tile + BN * l32 + 4 * ((8 * j + 2 * g + h) ^ (l32 & 7))) =
-                f32x4{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+            *reinterpret_cast<Sums *>(tile + BN * l32 + 4 * ((8 * j + 2 * g + h) ^ (l32 & 7))) =
+                Sums{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
     __syncthreads();
     for (int e = tid; e < 32 * BN / 2; e += 64 * WAVES) {
         const int row = e / (BN / 2), col = 2 * (e % (BN / 2));
         if (row >= t.rows || col >= out_cols) continue;
         const char *from = stages + 4 * (BN * row + 4 * ((col >> 2) ^ (row & 7)) + (col & 3));
-        float v0 = 0.0f, v1 = 0.0f;
+        Sum s0 = 0, s1 = 0;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const float *at = reinterpret_cast<const float *>(from + w * C::kStage);
-            v0 += at[0];
-            v1 += at[1];
+            const Sum *at = reinterpret_cast<const Sum *>(from + w * C::kStage);
+            s0 += at[0];
+            s1 += at[1];
         }
-        v0 *= p.alpha;
-        v1 *= p.alpha;
         const int64_t at = (int64_t)(row0 + row) * p.ldo + n0 + col;
         const bool both = col + 1 < out_cols;
+        float v0 = 0.0f, v1 = 0.0f;
+        if constexpr (C::I8) {
+            if (owner >= 0) {
+                const float sa = p.ts.a[(int64_t)(row0 + row) * p.ts.a_row];
+                const float *sb = p.ts.b + (int64_t)group * p.ts.b_group + (int64_t)(n0 + col) * p.ts.b_col;
+                const float *bias = p.ts.bias + (int64_t)group * p.ts.bias_group + n0 + col;
+                const bool with = p.ts.bias != nullptr;
+                v0 = int8_value((float)s0, sa, sb[0], with ? bias[0] : 0.0f);
+                if (both) v1 = int8_value((float)s1, sa, sb[p.ts.b_col], with ? bias[1] : 0.0f);
+            }
+        } else {
+            v0 = s0 * p.alpha;
+            v1 = s1 * p.alpha;
+        }
         if (p.out_type == GEMM_OUT_BF16) {
             uint16_t *o = static_cast<uint16_t *>(p.out) + at;
             o[0] = to_bf16(v0);
@@ -183,7 +197,7 @@ template <int DT, bool BKN, bool DMA> hipError_t launch(const GroupedParams &p, 
 }
 template <int DT> hipError_t launch_op(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t s) {
     if (op_b == GEMM_OP_T) return dma ? launch<DT, false, true>(p, s) : launch<DT, false, false>(p, s);
-    if constexpr (DT != GEMM_DTYPE_FP8F32)
+    if constexpr (DT != GEMM_DTYPE_FP8F32 && DT != kInt8)
         if (!dma) return launch<DT, true, false>(p, s);
     return launch<DT, true, true>(p, s);
 }
@@ -191,9 +205,9 @@ template <int DT> hipError_t launch_op(int32_t op_b, bool dma, const GroupedPara
 }  // namespace
 
 bool deep_takes(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p) {
+    // (128 columns of a slab, their fragments and the partial tile leave no registers to stage through.)
+    if ((dtype == GEMM_DTYPE_FP8F32 || dtype == kInt8) && op_b == GEMM_OP_N && !dma) return false;
     if (dtype == GEMM_DTYPE_FP8F32) {
-        // (128 columns of a slab, their fragments and the partial tile leave no registers to stage through.)
-        if (op_b == GEMM_OP_N && !dma) return false;
         const int64_t most = op_b == GEMM_OP_N ? 4864 : 4000;       // Deep::kScales
         if (((int64_t)p.K + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK * 32 > most) return false;
     }
@@ -204,6 +218,7 @@ bool deep_takes(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p) {
 hipError_t launch_grouped_deep(int32_t dtype, int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream) {
     if (dtype == GEMM_DTYPE_F32) return launch_op<GEMM_DTYPE_F32>(op_b, dma, p, stream);
     if (dtype == GEMM_DTYPE_BF16F32) return launch_op<GEMM_DTYPE_BF16F32>(op_b, dma, p, stream);
+    if (dtype == kInt8) return launch_op<kInt8>(op_b, dma, p, stream);
     return launch_op<GEMM_DTYPE_FP8F32>(op_b, dma, p, stream);
 }
 

@@ -1,18 +1,14 @@
-// Products of 8-bit integers with a scale for each token and channel.
-//
-// General kernel, for the calls that the tiles do not take: a row of an operand is shorter than one 16-byte
-// load, or rows lie so far apart that a tile's panel passes the 2 GiB a buffer load can address.  Every
+// Products of 8-bit integers with a scale for each token and channel: the tiles of gemm_grouped_tile.hpp with
+// 32-bit accumulators, and a general kernel, for the calls that those do not take: a row
+// of an operand is shorter than one 16-byte load, or rows lie so far apart that a tile's panel passes the 2 GiB a buffer load can address.  Every
 // layout, stride and alignment is right here.  An output tile of 64 x 64, 64 k of both operands staged a
 // byte at a time through registers into LDS as [row][k], four waves each keeping a quarter of the tile in 32-bit
 // accumulators, two v_mfma_i32_32x32x32_i8 a slab.  Such calls are bound by their results' stores, or by one
 // memory transaction a row.
-#include "gemm_grouped.hpp"
+#include "gemm_grouped_tile.hpp"
 
 namespace gemm {
 namespace {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int BT = 64, kBK = 64, kThreads = 256;
 constexpr int kStride = kBK + 16;            // bytes a panel row takes in LDS
@@ -67,7 +63,7 @@ int8_general_kernel(GroupedParams p, int tiles_n) {
         const int row = wm * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
         if (row >= t.rows) continue;
         const int64_t at = (int64_t)(row0 + row) * p.ldo + n0 + col;
-        const float v = scaled ? int8_value(acc[r], p.ts.a[(int64_t)(row0 + row) * p.ts.a_row], sb, bias) : bias;
+        const float v = scaled ? int8_value((float)acc[r], p.ts.a[(int64_t)(row0 + row) * p.ts.a_row], sb, bias) : bias;
         if (p.out_type == GEMM_OUT_BF16) static_cast<uint16_t *>(p.out)[at] = to_bf16(v);
         else static_cast<float *>(p.out)[at] = v;
     }
@@ -83,6 +79,10 @@ template <bool BN> hipError_t launch_general(const GroupedParams &p, hipStream_t
 }
 
 }  // namespace
+
+hipError_t launch_grouped_int8(int32_t op_b, bool dma, const GroupedParams &p, hipStream_t stream) {
+    return launch_typed<kInt8>(op_b, dma, p, stream);
+}
 
 hipError_t launch_int8_general(int32_t op_b, const GroupedParams &p, hipStream_t stream) {
     return op_b == GEMM_OP_N ? launch_general<true>(p, stream) : launch_general<false>(p, stream);

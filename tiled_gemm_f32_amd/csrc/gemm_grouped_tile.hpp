@@ -1,5 +1,5 @@
-// Tile kernel of the grouped and block-scaled products: instantiated in
-// gemm_grouped_f32.hip, gemm_grouped_bf16.hip and gemm_grouped_fp8.hip.
+// Tile kernel of the grouped and block-scaled products and of 8-bit integers: instantiated in
+// gemm_grouped_f32.hip, gemm_grouped_bf16.hip, gemm_grouped_fp8.hip and gemm_grouped_int8.hip.
 //
 // A workgroup makes a tile of BM x BN outputs of one group, walking k in
 // slabs of 128 bytes a row (32 fp32, 64 bf16 or 128 fp8 values: for fp8
@@ -54,6 +54,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "gemm_grouped.hpp"
 
@@ -62,7 +63,9 @@
 namespace gemm {
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 typedef unsigned __int128 u128;
@@ -80,7 +83,9 @@ struct TileConfig {
     static constexpr bool AKN = AKN_, BKN = BKN_, DMA = DMA_;
     static constexpr int NS = DMA ? NS_ : 2;          // LDS stages
     static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
-    static constexpr int esz = DT == GEMM_DTYPE_FP8F32 ? 1 : DT == GEMM_DTYPE_BF16F32 ? 2 : 4;
+    static constexpr bool I8 = DT == kInt8;
+    static constexpr int esz = I8 || DT == GEMM_DTYPE_FP8F32 ? 1 : DT == GEMM_DTYPE_BF16F32 ? 2 : 4;
+    typedef std::conditional_t<I8, i32x16, f32x16> Acc;      // one fragment pair's sums
     static constexpr int BK = kSlab / esz;            // k a slab
     // REG: slabs under way in registers.  Two where there is room: a small tile's products
     // of one slab do not cover a load.
@@ -285,6 +290,16 @@ __device__ __forceinline__ f32x16 product_f32(const FragOf<4> &a, const FragOf<4
     }
     return acc;
 }
+// 8-bit integers: the 64 k of an fp8 instruction as two of 32, each lane half's 32 consecutive ones split in
+// two alike in both operands.
+template <int ESZ>
+__device__ __forceinline__ i32x16 product(const FragOf<ESZ> &a, const FragOf<ESZ> &b, int half, i32x16 acc) {
+    const i32x8 av = a.h[half], bv = b.h[half];
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_shufflevector(bv, bv, 0, 1, 2, 3),
+                                                __builtin_shufflevector(av, av, 0, 1, 2, 3), acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_shufflevector(bv, bv, 4, 5, 6, 7),
+                                                 __builtin_shufflevector(av, av, 4, 5, 6, 7), acc, 0, 0, 0);
+}
 template <int ESZ>
 __device__ __forceinline__ f32x16 product(const FragOf<ESZ> &a, const FragOf<ESZ> &b, int half, f32x16 acc) {
     if constexpr (ESZ == 1) return product_fp8(a, b, half, acc);
@@ -375,11 +390,11 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
         return FP8 ? set[(wm * FM + i) * 32 + l32] * set[64 * kScaleA + wn * 32 * FN / GEMM_SCALE_BLOCK] : 0.0f;
     };
 
-    f32x16 acc[FM][FN];
+    typename C::Acc acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+        for (int j = 0; j < FN; ++j) acc[i][j] = typename C::Acc{};
     FragOf<C::esz> fa[2], fb[FN];
     static_assert(FM <= 2 || !C::AKN || C::esz == 2, "");
     uint32_t a_base = frag_base<C, C::AKN>(wm * FM, lane), b_base = frag_base<C, C::BKN>(wn * FN, lane);
@@ -586,6 +601,18 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
     const int el32 = elane & 31;
     const int cc = elane % kChunks;
     const int col = wn * 32 * FN + 4 * cc;
+    // 8-bit integers: the scales and the bias of this lane's columns.  (No k: rows past the last end, zeros.)
+    f32x4 col_scale = {}, col_bias = {};
+    if constexpr (C::I8) {
+        const float *sb = p.ts.b + (int64_t)group * p.ts.b_group + (int64_t)n0 * p.ts.b_col;
+        const float *bias = p.ts.bias + (int64_t)group * p.ts.bias_group + n0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (len > 0 && col + e < out_cols) {
+                col_scale[e] = sb[(col + e) * p.ts.b_col];
+                if (p.ts.bias != nullptr) col_bias[e] = bias[col + e];
+            }
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -594,7 +621,8 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
             for (int g = 0; g < 4; ++g) {
                 const int c = (8 * j + 2 * g + (elane >> 5)) ^ (el32 & (kChunks - 1));
                 *reinterpret_cast<f32x4 *>(piece + el32 * (kChunks * 16) + 16 * c) =
-                    f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                    f32x4{(float)acc[i][j][4 * g], (float)acc[i][j][4 * g + 1], (float)acc[i][j][4 * g + 2],
+                          (float)acc[i][j][4 * g + 3]};
             }
         constexpr int kRows = 64 / kChunks;          // rows an instruction takes
 #pragma unroll
@@ -605,8 +633,14 @@ __device__ __forceinline__ void make_tile(const GroupedParams &p, const Place &a
             if (row >= out_rows || col >= out_cols) continue;
             const int64_t o = (int64_t)row * p.ldo + col;
             const bool whole = col + 4 <= out_cols;
+            if constexpr (C::I8) {
+                const float row_scale = len > 0 ? p.ts.a[(int64_t)(row0 + row) * p.ts.a_row] : 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
+                for (int e = 0; e < 4; ++e) v[e] = int8_value(v[e], row_scale, col_scale[e], col_bias[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
+            }
             if (bf16_out) {
                 const uint32_t h0 = to_bf16(v[0]), h1 = to_bf16(v[1]), h2 = to_bf16(v[2]), h3 = to_bf16(v[3]);
                 if (whole) {
@@ -839,8 +873,8 @@ inline double deep_time(double rows, double cols, double slabs, double groups, i
 constexpr double kMatrixF32 = 1.75;
 
 template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParams &p, hipStream_t s) {
-    constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32, F32 = DT == GEMM_DTYPE_F32;
-    const double slabs = std::ceil((double)p.K * (FP8 ? 1 : F32 ? 4 : 2) / kSlab);
+    constexpr bool FP8 = DT == GEMM_DTYPE_FP8F32, F32 = DT == GEMM_DTYPE_F32, I8 = DT == kInt8;
+    const double slabs = std::ceil((double)p.K * (FP8 || I8 ? 1 : F32 ? 4 : 2) / kSlab);
     const double groups = p.ends != nullptr ? std::max(1, std::min(p.groups, p.M)) : 1;
     // Staging registers leave room for fewer accumulators, partial tiles for fewer still; fp32 is
     // bound by the matrix cores at 128 x 128 already.  (8 groups of 8000 x 4095 x 2047 bf16 through
@@ -862,7 +896,7 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
                 return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 4, false, BKN, DMA, DMA ? 3 : 2>>(p, s);
         case kTile128:
             // (The others' products of a 128 x 128 slab cover its loads.)
-            if constexpr (DMA && DT == GEMM_DTYPE_BF16F32)
+            if constexpr (DMA && (DT == GEMM_DTYPE_BF16F32 || I8))
                 if (c.turn) return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA, 4>>(p, s);
             if constexpr (first != kTile64)
                 return launch_grouped_tile<TileConfig<DT, 2, 2, 2, 2, false, BKN, DMA>>(p, s);
