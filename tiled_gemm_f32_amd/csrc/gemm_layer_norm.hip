@@ -39,16 +39,17 @@ __device__ __forceinline__ f32x8 unit_to_y(f32x8 c, float r, f32x8 w, f32x8 b) {
     return c;
 }
 
-template <int DT, int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
+template <int DT, int THREADS, int PER, bool LARGE>
+__global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS)
 layer_norm_kernel(LayerNormParams p) {
-    constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;
+    constexpr int TEAMS = THREADS == 64 ? 4 : 1;
     __shared__ float red[3 * (THREADS / 64)];
     const int64_t row = folded_block() * TEAMS + (TEAMS > 1 ? threadIdx.x / THREADS : 0);
     const int t = threadIdx.x % THREADS;
     if (row >= p.M) return;                    // the whole team together
     const int N = (int)p.N;
-    f32x8 s[PER], w[PER], b[PER];
+    f32x8 s[PER];
+    typename Io<DT>::Raw w[PER], b[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
@@ -57,16 +58,16 @@ layer_norm_kernel(LayerNormParams p) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        w[i] = load8<DT>(p.weight, col, N - col);
-        b[i] = f32x8{};
-        if (p.bias != nullptr) b[i] = load8<DT>(p.bias, col, N - col);
+        w[i] = load_raw<DT>(p.weight, col, N - col);
+        b[i] = {};
+        if (p.bias != nullptr) b[i] = load_raw<DT>(p.bias, col, N - col);
     }
     float total = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         total += sum8(s[i]);
         const int col = kChunk * (t + i * THREADS);
-        if (p.sum != nullptr) store8<DT>(p.sum, row * p.ld_sum + col, s[i], N - col);
+        if (p.sum != nullptr) store8<DT, LARGE>(p.sum, row * p.ld_sum + col, s[i], N - col);
     }
     const float mean = team_sum<THREADS>(total, red, 0) / (float)N;
     float sq = 0.0f;
@@ -81,9 +82,9 @@ layer_norm_kernel(LayerNormParams p) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int col = kChunk * (t + i * THREADS);
-        s[i] = unit_to_y(s[i], r, w[i], b[i]);
+        s[i] = unit_to_y(s[i], r, Io<DT>::values(w[i]), Io<DT>::values(b[i]));
         if (p.out_type == GEMM_OUT_INT8) top = max(top, max_bits(s[i]));     // (zero past the row's end)
-        else put_norm(p, row, col, s[i], N - col);
+        else put_norm<LARGE>(p, row, col, s[i], N - col);
     }
     if (p.out_type != GEMM_OUT_INT8) return;
     top = team_max<THREADS>(top, red, 2);
@@ -169,10 +170,10 @@ template <int THREADS> __device__ __forceinline__ void team_sum2(float &a, float
 // A first trip around the team sums s and g, a second c^2 and g * c.  As in gemm_norm.hip a team takes rows
 // team, team + teams, ... and keeps its columns' weights and both gradient sums in registers; they go to a
 // row of `partials` each (N of dweight, then N of dbias), which layer_dweight_kernel adds.
-template <int DT, int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
+template <int DT, int THREADS, int PER, bool LARGE>
+__global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS)
 layer_norm_backward_kernel(LayerNormGradParams p) {
-    constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;
+    constexpr int TEAMS = THREADS == 64 ? 4 : 1;
     typedef typename Io<DT>::Raw Raw;
     __shared__ float red[4 * (THREADS / 64)];
     const int team = blockIdx.x * TEAMS + (TEAMS > 1 ? threadIdx.x / THREADS : 0), teams = gridDim.x * TEAMS;
@@ -192,9 +193,9 @@ layer_norm_backward_kernel(LayerNormGradParams p) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int col = kChunk * (t + i * THREADS);
-            s[i] = load_raw<DT>(p.s, row * p.lds + col, N - col);
-            dy[i] = load_raw<DT>(p.dy, row * p.lddy + col, N - col);
-            if (p.ds != nullptr) ds[i] = load_raw<DT>(p.ds, row * p.ldds + col, N - col);
+            s[i] = load_raw<DT, LARGE>(p.s, row * p.lds + col, N - col);
+            dy[i] = load_raw<DT, LARGE>(p.dy, row * p.lddy + col, N - col);
+            if (p.ds != nullptr) ds[i] = load_raw<DT, LARGE>(p.ds, row * p.ldds + col, N - col);
         }
         float total = 0.0f, g_sum = 0.0f;
 #pragma unroll
@@ -232,7 +233,7 @@ layer_norm_backward_kernel(LayerNormGradParams p) {
                 dw[i][e] = fmaf(yv[e], n, dw[i][e]);
                 db[i][e] += yv[e];
             }
-            store8<DT>(p.dx, row * p.lddx + col, dx, N - col);
+            store8<DT, LARGE>(p.dx, row * p.lddx + col, dx, N - col);
         }
     }
     if (p.partials == nullptr) return;
@@ -262,8 +263,8 @@ layer_norm_backward_kernel(LayerNormGradParams p) {
     }
 }
 
-// Rows past 16384 values (8192 in fp32): the sums first, then the row again from the caches.  The
-// gradients' running sums live in `partials`.
+// Rows past 16384 values: the sums first, then the row again from the caches.  The gradients' running sums
+// live in `partials`.
 template <int DT>
 __global__ void __launch_bounds__(1024)
 layer_norm_backward_long_kernel(LayerNormGradParams p) {
@@ -351,9 +352,9 @@ layer_dweight_kernel(const float *partials, float *dweight, float *dbias, int pa
 
 // Codes of rows with a scale each.
 template <int DT, int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
+__global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS)
 quantize_int8_kernel(Int8Params p) {
-    constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;
+    constexpr int TEAMS = THREADS == 64 ? 4 : 1;
     __shared__ float red[THREADS / 64];
     const int64_t row = folded_block() * TEAMS + (TEAMS > 1 ? threadIdx.x / THREADS : 0);
     const int t = threadIdx.x % THREADS;
@@ -397,36 +398,34 @@ quantize_int8_long_kernel(Int8Params p) {
     if (threadIdx.x == 0) p.scales[row] = scale;
 }
 
-template <int DT> hipError_t norm_type(const LayerNormParams &p, hipStream_t s) {
-    switch (shape_of(p.N)) {
-        case kWave2: return go(&layer_norm_kernel<DT, 64, 2>, fold((p.M + 3) / 4), 256, s, p);
-        case kFour2: return go(&layer_norm_kernel<DT, 256, 2>, fold(p.M), 256, s, p);
-        case kSixteen1: return go(&layer_norm_kernel<DT, 1024, 1>, fold(p.M), 1024, s, p);
-        case kSixteen2: return go(&layer_norm_kernel<DT, 1024, 2>, fold(p.M), 1024, s, p);
-        default: return go(&layer_norm_long_kernel<DT>, fold(p.M), 1024, s, p);
-    }
+// A chunk a lane keeps the most rows' loads under way.  8192 rows in 512 threads and one chunk, and in 256 and
+// two: 4096 bf16 50 us and 53; in 1024 and one, and 512 and two: 8192 bf16 92 and 97, but 94 and 86 to codes with
+// a scale a row, which take another trip around the team.
+template <int DT, bool LARGE> hipError_t norm_type(const LayerNormParams &p, hipStream_t s) {
+    if (p.N <= 1024) return go(&layer_norm_kernel<DT, 64, 2, LARGE>, fold((p.M + 3) / 4), 256, s, p);
+    if (p.N <= 2048) return go(&layer_norm_kernel<DT, 256, 1, LARGE>, fold(p.M), 256, s, p);
+    if (p.N <= 4096) return go(&layer_norm_kernel<DT, 512, 1, LARGE>, fold(p.M), 512, s, p);
+    if (p.N <= 8192 && p.out_type == GEMM_OUT_INT8) return go(&layer_norm_kernel<DT, 512, 2, LARGE>, fold(p.M), 512, s, p);
+    if (p.N <= 8192) return go(&layer_norm_kernel<DT, 1024, 1, LARGE>, fold(p.M), 1024, s, p);
+    if (p.N <= 16384) return go(&layer_norm_kernel<DT, 1024, 2, LARGE>, fold(p.M), 1024, s, p);
+    return go(&layer_norm_long_kernel<DT>, fold(p.M), 1024, s, p);
 }
 
-// Workgroups of the backward pass, as in gemm_norm.hip.
+// Workgroups of the backward pass: enough to fill the compute units with teams that each still take several
+// rows, so that the partial sums stay a small part of what is moved.
 int grad_workgroups(int64_t M, int64_t N) {
-    const Shape sh = shape_of(N);
-    const int64_t rows = sh == kWave2 ? (M + 3) / 4 : M;     // rows a workgroup takes at once: 4, or 1
-    const int64_t most = sh == kFour2 ? 768 : 512;
-    return (int)(rows < most ? rows : most);
+    const int64_t rows = N <= 1024 ? (M + 3) / 4 : M;        // rows a workgroup takes at once: 4, or 1
+    return (int)(rows < 512 ? rows : 512);
 }
 
-template <int DT> hipError_t grad_type(const LayerNormGradParams &p, hipStream_t s) {
+// (8192 x 8192 bf16 in 1024 threads and one chunk 114 us, in 512 and two 102.)
+template <int DT, bool LARGE> hipError_t grad_type(const LayerNormGradParams &p, hipStream_t s) {
     const dim3 grid((unsigned)grad_workgroups(p.M, p.N));
-    Shape sh = shape_of(p.N);
-    // Two chunks a lane of everything the backward pass holds do not fit the 128 registers that sixteen
-    // waves leave each.
-    if (sh == kSixteen2) sh = kLong;
-    switch (sh) {
-        case kWave2: return go(&layer_norm_backward_kernel<DT, 64, 2>, grid, 256, s, p);
-        case kFour2: return go(&layer_norm_backward_kernel<DT, 256, 2>, grid, 256, s, p);
-        case kSixteen1: return go(&layer_norm_backward_kernel<DT, 1024, 1>, grid, 1024, s, p);
-        default: return go(&layer_norm_backward_long_kernel<DT>, grid, 1024, s, p);
-    }
+    if (p.N <= 1024) return go(&layer_norm_backward_kernel<DT, 64, 2, LARGE>, grid, 256, s, p);
+    if (p.N <= 4096) return go(&layer_norm_backward_kernel<DT, 256, 2, LARGE>, grid, 256, s, p);
+    if (p.N <= 8192) return go(&layer_norm_backward_kernel<DT, 512, 2, LARGE>, grid, 512, s, p);
+    if (p.N <= 16384) return go(&layer_norm_backward_kernel<DT, 512, 4, LARGE>, grid, 512, s, p);
+    return go(&layer_norm_backward_long_kernel<DT>, grid, 1024, s, p);
 }
 
 template <int DT> hipError_t quantize_type(const Int8Params &p, hipStream_t s) {
@@ -446,15 +445,29 @@ int layer_norm_grad_partials(int64_t M, int64_t N) {
     return grad_workgroups(M, N);
 }
 
+// A pass whose operands of this many bytes each cannot stay in the L2 goes past it (8192 x 4096 bf16: forward 51 us
+// and 50 so, backward 57 and 51).
+static bool large(int64_t M, int64_t N, int32_t dtype) { return (double)M * N * (dtype == GEMM_DTYPE_F32 ? 4 : 2) >= 32 << 20; }
+
 hipError_t launch_layer_norm(const LayerNormParams &p, hipStream_t s) {
-    return p.dtype == GEMM_DTYPE_F32 ? norm_type<GEMM_DTYPE_F32>(p, s) : norm_type<GEMM_DTYPE_BF16F32>(p, s);
+    if (large(p.M, p.N, p.dtype))
+        return p.dtype == GEMM_DTYPE_F32 ? norm_type<GEMM_DTYPE_F32, true>(p, s)
+                                         : norm_type<GEMM_DTYPE_BF16F32, true>(p, s);
+    return p.dtype == GEMM_DTYPE_F32 ? norm_type<GEMM_DTYPE_F32, false>(p, s)
+                                     : norm_type<GEMM_DTYPE_BF16F32, false>(p, s);
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormGradParams &p, hipStream_t s) {
     const bool sums = p.dweight != nullptr || p.dbias != nullptr;
     hipError_t err = hipSuccess;
-    if (p.M > 0)
-        err = p.dtype == GEMM_DTYPE_F32 ? grad_type<GEMM_DTYPE_F32>(p, s) : grad_type<GEMM_DTYPE_BF16F32>(p, s);
+    if (p.M > 0) {
+        if (large(p.M, p.N, p.dtype))
+            err = p.dtype == GEMM_DTYPE_F32 ? grad_type<GEMM_DTYPE_F32, true>(p, s)
+                                            : grad_type<GEMM_DTYPE_BF16F32, true>(p, s);
+        else
+            err = p.dtype == GEMM_DTYPE_F32 ? grad_type<GEMM_DTYPE_F32, false>(p, s)
+                                            : grad_type<GEMM_DTYPE_BF16F32, false>(p, s);
+    }
     if (err != hipSuccess || !sums) return err;
     return go(&layer_dweight_kernel, fold((2 * p.N + 31) / 32), 1024, s, (const float *)p.partials, p.dweight, p.dbias,
               layer_norm_grad_partials(p.M, p.N), p.N);

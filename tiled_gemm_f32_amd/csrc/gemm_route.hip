@@ -54,20 +54,31 @@ __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
     return m;
 }
 
+// `waves`: those that have a table of counts, and choices; with more workgroups than one, the others help to
+// add up their counts.
 __global__ void __launch_bounds__(1024)
-plan_place_kernel(PlanParams p, int bits) {
+plan_place_kernel(PlanParams p, int bits, int waves) {
     extern __shared__ __attribute__((aligned(16))) int lds[];
     __shared__ int used;
     const int E = p.groups, tid = threadIdx.x, threads = blockDim.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     volatile int *count = lds;                 // [waves][E]: choices, then the next row of each expert
     volatile int *start = lds + waves * E;     // [E]
-    for (int i = tid; i < waves * E; i += threads) count[i] = 0;
+    int *before = lds + (waves + 1) * E;       // [E]: choices of the workgroups before (more than one only)
+    const int tables = (p.blocks > 1 ? waves + 2 : waves + 1) * E;
+    for (int i = tid; i < tables; i += threads) count[i] = 0;
     __syncthreads();
+    if (p.blocks > 1)
+        for (int i = tid; i < p.blocks * E; i += threads) {
+            const int b = i / E, e = i - b * E, c = p.counts[i];
+            if (c == 0) continue;
+            atomicAdd(&lds[waves * E + e], c);
+            if (b < (int)blockIdx.x) atomicAdd(&before[e], c);
+        }
 
     const int first = blockIdx.x * p.per, mine = max(0, min(p.choices - first, p.per));
     const int each = ((mine + waves - 1) / waves + 63) / 64 * 64;
-    const int lo = first + min(mine, wave * each), hi = first + min(mine, (wave + 1) * each);
+    const int lo = first + min(mine, wave * each), hi = wave < waves ? first + min(mine, (wave + 1) * each) : lo;
     for (int i = lo + lane; i < hi; i += 64) {
         const int e = expert_of(p, i);
         if (e >= 0) atomicAdd(&lds[wave * E + e], 1);
@@ -77,19 +88,13 @@ plan_place_kernel(PlanParams p, int bits) {
     // A wave's first row of an expert, counted from the expert's start: the choices of the workgroups and
     // of the waves before.
     for (int e = tid; e < E; e += threads) {
-        int run = 0, all = 0;
-        if (p.blocks > 1)
-            for (int b = 0; b < p.blocks; ++b) {
-                const int c = p.counts[(int64_t)b * E + e];
-                run += b < (int)blockIdx.x ? c : 0;
-                all += c;
-            }
+        int run = p.blocks > 1 ? before[e] : 0;
         for (int w = 0; w < waves; ++w) {
             const int c = count[w * E + e];
             count[w * E + e] = run;
             run += c;
         }
-        start[e] = p.blocks > 1 ? all : run;
+        if (p.blocks == 1) start[e] = run;
     }
     __syncthreads();
     if (wave == 0) {
@@ -151,7 +156,7 @@ __device__ __forceinline__ int64_t wave_unit(int64_t first) {
 // A wave holds 1024 * U bytes of a token's row and stores them to each of its rows.  A row's last 16 bytes
 // end where it does, over what the 16 before hold: the bytes in both are the same.  `teams`: tokens, or as
 // many waves as clear the rows past the last group's where there are none.
-template <int U>
+template <int U, bool LARGE>
 __global__ void __launch_bounds__(256)
 dispatch_kernel(DispatchParams p, int64_t teams, int slabs) {
     const int64_t u = wave_unit(folded_block());
@@ -169,7 +174,9 @@ dispatch_kernel(DispatchParams p, int64_t teams, int slabs) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int64_t at = first + 1024 * i + 16 * lane;
-                if (at < p.wide) put(to + min(at, p.wide - 16), v[i]);
+                if (at >= p.wide) continue;
+                if (LARGE) put_nt(to + min(at, p.wide - 16), v[i]);
+                else put(to + min(at, p.wide - 16), v[i]);
             }
         } else if (lane < p.wide) {
             to[lane] = (char)v[0][0];
@@ -205,8 +212,9 @@ dispatch_kernel(DispatchParams p, int64_t teams, int slabs) {
 }
 
 // A wave makes 512 values of a token: the residual's, then each choice's in turn times its weight, in fp32.
-// Four choices' loads are under way at a time.
-template <int DT>
+// Its lanes read the places and weights of up to 64 choices at once; of those that have a row, four rows'
+// loads are under way at a time.
+template <int DT, bool LARGE>
 __global__ void __launch_bounds__(256)
 combine_kernel(CombineParams p, int slabs) {
     typedef typename Io<DT>::Raw Raw;
@@ -215,36 +223,47 @@ combine_kernel(CombineParams p, int slabs) {
     int64_t token;
     int slab;
     split_unit(u, slabs, token, slab);
-    const int64_t col = (int64_t)slab * 512 + kChunk * (threadIdx.x & 63);
+    const int lane = threadIdx.x & 63;
+    const int64_t col = (int64_t)slab * 512 + kChunk * lane;
     const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.N - col));
     f32x8 acc = {};
     if (p.residual != nullptr) acc = load8<DT>(p.residual, token * p.ld_res + col, n);
-    for (int k0 = 0; k0 < p.top; k0 += 4) {
-        Raw v[4];
-        int row[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            row[j] = k0 + j < p.top ? p.place[token * p.top + k0 + j] : -1;
-            if (row[j] >= p.n_rows) row[j] = -1;
-            v[j] = Raw{};
-            if (row[j] >= 0) v[j] = load_raw<DT>(p.rows, row[j] * p.ldr + col, n);
+    for (int k0 = 0; k0 < p.top; k0 += 64) {
+        int place = -1;
+        float share = 1.0f;
+        if (k0 + lane < p.top) {
+            place = p.place[token * p.top + k0 + lane];
+            if (p.weights != nullptr) share = p.weights[token * p.ldw + k0 + lane];
         }
+        uint64_t left = __ballot(place >= 0 && place < p.n_rows);
+        while (left != 0) {
+            Raw v[4];
+            float w[4];
+            const int many = min(__popcll(left), 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (row[j] < 0) continue;
-            const float w = p.weights != nullptr ? p.weights[token * p.ldw + k0 + j] : 1.0f;
-            const f32x8 f = Io<DT>::values(v[j]);
+            for (int j = 0; j < 4; ++j) {
+                if (j >= many) continue;
+                const int k = __ffsll((unsigned long long)left) - 1;
+                left &= left - 1;
+                w[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, share), k));
+                v[j] = load_raw<DT, LARGE>(p.rows, (int64_t)__builtin_amdgcn_readlane(place, k) * p.ldr + col, n);
+            }
 #pragma unroll
-            for (int e = 0; e < kChunk; ++e) acc[e] = fmaf(w, f[e], acc[e]);
+            for (int j = 0; j < 4; ++j) {
+                if (j >= many) continue;
+                const f32x8 f = Io<DT>::values(v[j]);
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
+            }
         }
     }
-    store8<DT>(p.out, token * p.ldo + col, acc, n);
+    store8<DT, LARGE>(p.out, token * p.ldo + col, acc, n);
 }
 
 // Gradients of combine: a team of threads holds a token's dout, and for each of its choices stores weight *
 // dout to the choice's row and sums dout * the row.  LONG: rows that the team walks.
 constexpr int kGradChoices = 64;          // choices whose sums wait in LDS
-template <int DT, int THREADS, int PER, bool LONG>
+template <int DT, int THREADS, int PER, bool LONG, bool LARGE>
 __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
 combine_backward_kernel(CombineGradParams p, int64_t teams) {
     constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1, W = THREADS / 64;
@@ -261,7 +280,7 @@ combine_backward_kernel(CombineGradParams p, int64_t teams) {
         for (int i = 0; i < PER; ++i) {
             const int64_t col = c0 + kChunk * (t + i * THREADS);
             const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.N - col));
-            d[i] = load_raw<DT>(p.dout, token * p.lddo + col, n);
+            d[i] = load_raw<DT, LARGE>(p.dout, token * p.lddo + col, n);
         }
     };
     if (token < p.tokens) {
@@ -282,7 +301,7 @@ combine_backward_kernel(CombineGradParams p, int64_t teams) {
                             const int64_t col = c0 + kChunk * (t + i * THREADS);
                             const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.N - col));
                             v[i] = Raw{};
-                            if (p.dweights != nullptr) v[i] = load_raw<DT>(p.rows, row * p.ldr + col, n);
+                            if (p.dweights != nullptr) v[i] = load_raw<DT, LARGE>(p.rows, row * p.ldr + col, n);
                         }
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
@@ -295,7 +314,7 @@ combine_backward_kernel(CombineGradParams p, int64_t teams) {
                                 s = fmaf(g[e], f[e], s);
                                 g[e] *= w;
                             }
-                            store8<DT>(p.drows, row * p.lddr + col, g, n);
+                            store8<DT, LARGE>(p.drows, row * p.lddr + col, g, n);
                         }
                     }
                 }
@@ -326,7 +345,7 @@ combine_backward_kernel(CombineGradParams p, int64_t teams) {
             for (int i = 0; i < PER; ++i) {
                 const int64_t col = c0 + kChunk * (t + i * THREADS);
                 const int n = (int)max((int64_t)0, min((int64_t)kChunk, p.N - col));
-                store8<DT>(p.drows, row * p.lddr + col, f32x8{}, n);
+                store8<DT, LARGE>(p.drows, row * p.lddr + col, f32x8{}, n);
             }
         }
 }
@@ -336,19 +355,22 @@ int64_t teams_for(int64_t tokens, int64_t rows, bool clears) {
     return tokens > 0 || !clears ? tokens : rows < 1024 ? rows : 1024;
 }
 
-template <int DT> hipError_t combine_type(const CombineParams &p, hipStream_t s) {
+// Rows of so many bytes in all cannot stay in the L2: they go past it.
+bool large(int64_t rows, int64_t bytes) { return (double)rows * bytes >= 32 << 20; }
+
+template <int DT, bool LARGE> hipError_t combine_type(const CombineParams &p, hipStream_t s) {
     const int slabs = (int)((p.N + 511) / 512);
-    return go(&combine_kernel<DT>, fold((p.tokens * slabs + 3) / 4), 256, s, p, slabs);
+    return go(&combine_kernel<DT, LARGE>, fold((p.tokens * slabs + 3) / 4), 256, s, p, slabs);
 }
 
-template <int DT> hipError_t combine_grad_type(const CombineGradParams &p, hipStream_t s) {
+template <int DT, bool LARGE> hipError_t combine_grad_type(const CombineGradParams &p, hipStream_t s) {
     const int64_t teams = teams_for(p.tokens, p.n_rows, p.last != nullptr);
     if (teams == 0) return hipSuccess;
     switch (shape_of(p.N)) {
-        case kWave2: return go(&combine_backward_kernel<DT, 64, 2, false>, fold((teams + 3) / 4), 256, s, p, teams);
-        case kFour2: return go(&combine_backward_kernel<DT, 256, 2, false>, fold(teams), 256, s, p, teams);
-        case kSixteen1: return go(&combine_backward_kernel<DT, 1024, 1, false>, fold(teams), 1024, s, p, teams);
-        default: return go(&combine_backward_kernel<DT, 1024, 1, true>, fold(teams), 1024, s, p, teams);
+        case kWave2: return go(&combine_backward_kernel<DT, 64, 2, false, LARGE>, fold((teams + 3) / 4), 256, s, p, teams);
+        case kFour2: return go(&combine_backward_kernel<DT, 256, 2, false, LARGE>, fold(teams), 256, s, p, teams);
+        case kSixteen1: return go(&combine_backward_kernel<DT, 1024, 1, false, LARGE>, fold(teams), 1024, s, p, teams);
+        default: return go(&combine_backward_kernel<DT, 1024, 1, true, LARGE>, fold(teams), 1024, s, p, teams);
     }
 }
 
@@ -365,8 +387,9 @@ hipError_t launch_plan(const PlanParams &p, hipStream_t s) {
     PlanParams q = p;
     q.blocks = plan_blocks(p.choices);
     q.per = (p.choices + q.blocks - 1) / q.blocks;
+    // As many waves as have 64 choices, and as their tables leave room for.
     int waves = 16;
-    while (waves * p.groups > kPlanCounters) waves /= 2;       // (2 at least)
+    while (waves > 1 && (waves * p.groups > kPlanCounters || 32 * waves >= q.per)) waves /= 2;
     int bits = 1;
     while (p.groups >> bits != 0) ++bits;
     if (q.blocks > 1) {
@@ -375,9 +398,10 @@ hipError_t launch_plan(const PlanParams &p, hipStream_t s) {
                                                dim3(1024), argv, (size_t)q.groups * 4, s);
         if (err != hipSuccess) return err;
     }
-    void *argv[] = {&q, &bits};
+    void *argv[] = {&q, &bits, &waves};
     return hipLaunchKernel(reinterpret_cast<const void *>(&plan_place_kernel), dim3((unsigned)q.blocks),
-                           dim3((unsigned)(64 * waves)), argv, (size_t)(waves + 1) * q.groups * 4, s);
+                           dim3((unsigned)(q.blocks > 1 ? 1024 : 64 * waves)), argv,
+                           (size_t)(q.blocks > 1 ? waves + 2 : waves + 1) * q.groups * 4, s);
 }
 
 hipError_t launch_dispatch(const DispatchParams &p, hipStream_t s) {
@@ -385,17 +409,29 @@ hipError_t launch_dispatch(const DispatchParams &p, hipStream_t s) {
     if (teams == 0) return hipSuccess;
     // 4 KB a wave where that leaves waves for every compute unit, else 1 KB.
     const int big = (int)((p.wide + 4095) / 4096), small = (int)((p.wide + 1023) / 1024);
-    if (teams * big >= 4096) return go(&dispatch_kernel<4>, fold((teams * big + 3) / 4), 256, s, p, teams, big);
-    return go(&dispatch_kernel<1>, fold((teams * small + 3) / 4), 256, s, p, teams, small);
+    const bool wide = teams * big >= 4096;
+    const dim3 grid = fold((teams * (wide ? big : small) + 3) / 4);
+    if (large(p.rows, p.wide))
+        return wide ? go(&dispatch_kernel<4, true>, grid, 256, s, p, teams, big)
+                    : go(&dispatch_kernel<1, true>, grid, 256, s, p, teams, small);
+    return wide ? go(&dispatch_kernel<4, false>, grid, 256, s, p, teams, big)
+                : go(&dispatch_kernel<1, false>, grid, 256, s, p, teams, small);
 }
 
 hipError_t launch_combine(const CombineParams &p, hipStream_t s) {
-    return p.dtype == GEMM_DTYPE_F32 ? combine_type<GEMM_DTYPE_F32>(p, s) : combine_type<GEMM_DTYPE_BF16F32>(p, s);
+    if (large(p.n_rows, p.N * (p.dtype == GEMM_DTYPE_F32 ? 4 : 2)))
+        return p.dtype == GEMM_DTYPE_F32 ? combine_type<GEMM_DTYPE_F32, true>(p, s)
+                                         : combine_type<GEMM_DTYPE_BF16F32, true>(p, s);
+    return p.dtype == GEMM_DTYPE_F32 ? combine_type<GEMM_DTYPE_F32, false>(p, s)
+                                     : combine_type<GEMM_DTYPE_BF16F32, false>(p, s);
 }
 
 hipError_t launch_combine_backward(const CombineGradParams &p, hipStream_t s) {
-    return p.dtype == GEMM_DTYPE_F32 ? combine_grad_type<GEMM_DTYPE_F32>(p, s)
-                                     : combine_grad_type<GEMM_DTYPE_BF16F32>(p, s);
+    if (large(p.n_rows, p.N * (p.dtype == GEMM_DTYPE_F32 ? 4 : 2)))
+        return p.dtype == GEMM_DTYPE_F32 ? combine_grad_type<GEMM_DTYPE_F32, true>(p, s)
+                                         : combine_grad_type<GEMM_DTYPE_BF16F32, true>(p, s);
+    return p.dtype == GEMM_DTYPE_F32 ? combine_grad_type<GEMM_DTYPE_F32, false>(p, s)
+                                     : combine_grad_type<GEMM_DTYPE_BF16F32, false>(p, s);
 }
 
 }  // namespace gemm

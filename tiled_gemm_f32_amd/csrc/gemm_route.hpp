@@ -47,8 +47,8 @@ struct CombineGradParams {
 };
 
 constexpr int64_t kPlanGroups = 4096, kPlanChoices = int64_t(1) << 30;
-// Counters of a workgroup's waves, a table of the groups each: with one table more they fit 64 KB of LDS.
-constexpr int kPlanCounters = 12288;
+// Counters of a workgroup's waves, a table of the groups each: with two tables more they fit 64 KB of LDS.
+constexpr int kPlanCounters = 8000;
 // Workgroups that sort so many choices (1: one launch and no workspace).
 int plan_blocks(int64_t choices);
 

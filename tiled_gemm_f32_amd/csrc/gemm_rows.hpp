@@ -47,16 +47,25 @@ template <class V> __device__ __forceinline__ V get(const void *p) {
     return reinterpret_cast<const Anywhere<V> *>(p)->v;
 }
 template <class V> __device__ __forceinline__ void put(void *p, V v) { reinterpret_cast<Anywhere<V> *>(p)->v = v; }
+// The same past the L2, which would hold them until something else pushes them out.
+template <class V> __device__ __forceinline__ V get_nt(const void *p) {
+    typedef V Loose __attribute__((aligned(1)));
+    return __builtin_nontemporal_load(static_cast<const Loose *>(p));
+}
+template <class V> __device__ __forceinline__ void put_nt(void *p, V v) {
+    typedef V Loose __attribute__((aligned(1)));
+    __builtin_nontemporal_store(v, static_cast<Loose *>(p));
+}
 
 // Up to 8 values, n of them valid (n <= 0: none; the rest read as zero).
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ typename Io<DT>::Raw load_raw(const void *base, int64_t at, int n) {
     typedef typename Io<DT>::T T;
     typedef typename Io<DT>::Raw Raw;
     const T *src = static_cast<const T *>(base) + at;
     Raw r = {};
     if (n >= kChunk) {
-        r = get<Raw>(src);
+        r = NT ? get_nt<Raw>(src) : get<Raw>(src);
     } else if constexpr (DT == GEMM_DTYPE_F32) {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e)
@@ -72,18 +81,20 @@ template <int DT>
 __device__ __forceinline__ f32x8 load8(const void *base, int64_t at, int n) {
     return Io<DT>::values(load_raw<DT>(base, at, n));
 }
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(void *base, int64_t at, f32x8 v, int n) {
     typedef typename Io<DT>::T T;
     T *dst = static_cast<T *>(base) + at;
     if (n >= kChunk) {
         if constexpr (DT == GEMM_DTYPE_F32) {
-            put(dst, v);
+            if constexpr (NT) put_nt(dst, v);
+            else put(dst, v);
         } else {
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = (uint32_t)to_bf16(v[2 * i]) | ((uint32_t)to_bf16(v[2 * i + 1]) << 16);
-            put(dst, w);
+            if constexpr (NT) put_nt(dst, w);
+            else put(dst, w);
         }
     } else {
 #pragma unroll
@@ -168,7 +179,7 @@ template <int THREADS> __device__ __forceinline__ float team_sum(float v, float 
 
 // One chunk's y out: fp32, bf16, or codes with their block's scale.  A chunk
 // that is wholly past the row's end takes part in the lane rotations only.
-template <class P>
+template <bool NT = false, class P>
 __device__ __forceinline__ void put_norm(const P &p, int64_t row, int64_t col, f32x8 y, int n) {
     if (p.out_type == GEMM_OUT_FP8) {
         const float amax = fmaxf(max16(finite_max(y)), kMinAmax);
@@ -179,9 +190,9 @@ __device__ __forceinline__ void put_norm(const P &p, int64_t row, int64_t col, f
                 p.scales[row * p.ld_scales + col / GEMM_SCALE_BLOCK] = amax / kE4m3Max;
         }
     } else if (p.out_type == GEMM_OUT_BF16) {
-        store8<GEMM_DTYPE_BF16F32>(p.out, row * p.ldo + col, y, n);
+        store8<GEMM_DTYPE_BF16F32, NT>(p.out, row * p.ldo + col, y, n);
     } else {
-        store8<GEMM_DTYPE_F32>(p.out, row * p.ldo + col, y, n);
+        store8<GEMM_DTYPE_F32, NT>(p.out, row * p.ldo + col, y, n);
     }
 }
 
