@@ -10,6 +10,8 @@
 // The others are passes over rows, bound by HBM.  All go by token, not by row: a token's row is read once
 // and written to each of its experts' rows, or its experts' rows are read and it is written once, so that
 // no sum needs an atomic and none is made in an order that could change.
+#include <algorithm>
+
 #include "gemm_route.hpp"
 #include "gemm_rows.hpp"
 
@@ -68,13 +70,21 @@ plan_place_kernel(PlanParams p, int bits, int waves) {
     const int tables = (p.blocks > 1 ? waves + 2 : waves + 1) * E;
     for (int i = tid; i < tables; i += threads) count[i] = 0;
     __syncthreads();
-    if (p.blocks > 1)
-        for (int i = tid; i < p.blocks * E; i += threads) {
-            const int b = i / E, e = i - b * E, c = p.counts[i];
-            if (c == 0) continue;
-            atomicAdd(&lds[waves * E + e], c);
-            if (b < (int)blockIdx.x) atomicAdd(&before[e], c);
+    if (p.blocks > 1) {
+        // Threads share out an expert's column of the counts where there are fewer experts than threads.
+        const int wide = bits < 10 ? 1 << bits : 1024, part = tid / wide, parts = threads / wide;
+        for (int e = tid & (wide - 1); e < E; e += wide) {
+            int all = 0, run = 0;
+#pragma unroll 8
+            for (int b = part; b < p.blocks; b += parts) {
+                const int c = p.counts[(int64_t)b * E + e];
+                all += c;
+                run += b < (int)blockIdx.x ? c : 0;
+            }
+            atomicAdd(&lds[waves * E + e], all);
+            atomicAdd(&before[e], run);
         }
+    }
 
     const int first = blockIdx.x * p.per, mine = max(0, min(p.choices - first, p.per));
     const int each = ((mine + waves - 1) / waves + 63) / 64 * 64;
@@ -376,11 +386,11 @@ template <int DT, bool LARGE> hipError_t combine_grad_type(const CombineGradPara
 
 }  // namespace
 
-// One workgroup up to 8192 choices, eight steps a wave; at most 64, whose counts each of them then reads.
+// One workgroup for few choices: a second launch costs as much as four steps of its waves (2048 choices of 64
+// groups 6.2 us in one, 6.8 in five; 8192 of 128 groups 14.0 and 8.2).  Each of several then adds up the counts
+// of all, which bounds how many pay (65536 of 64: 8.4 us in 64, 7.9 in 128; 524288: 18.2 and 13.4).
 int plan_blocks(int64_t choices) {
-    if (choices <= 8192) return 1;
-    const int64_t b = (choices + 1023) / 1024;
-    return (int)(b < 64 ? b : 64);
+    return choices <= 2048 ? 1 : (int)std::min((choices + 511) / 512, (int64_t)128);
 }
 
 hipError_t launch_plan(const PlanParams &p, hipStream_t s) {
