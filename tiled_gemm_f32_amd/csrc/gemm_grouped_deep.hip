@@ -136,6 +136,25 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     if (mine > 0) step(mine - 1, true);
 
     // Partial tiles: row l32 of 8 * FN chunks of 4 columns, chunk c at c ^ (row & 7).
+    // 8-bit integers: the scales and the bias of this thread's results, under way while the sums are added.  Its
+    // results are all of two columns.
+    constexpr int kTurns = (32 * BN / 2 + 64 * WAVES - 1) / (64 * WAVES);
+    static_assert(64 * WAVES % (BN / 2) == 0, "");
+    float row_scale[kTurns] = {}, col_scale[2] = {}, col_bias[2] = {};
+    if (C::I8 && owner >= 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int col = 2 * (tid % (BN / 2)) + c;
+            if (col >= out_cols) continue;
+            col_scale[c] = p.ts.b[(int64_t)group * p.ts.b_group + (int64_t)(n0 + col) * p.ts.b_col];
+            if (p.ts.bias != nullptr) col_bias[c] = p.ts.bias[(int64_t)group * p.ts.bias_group + n0 + col];
+        }
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int row = (tid + u * 64 * WAVES) / (BN / 2);
+            if (row < t.rows) row_scale[u] = p.ts.a[(int64_t)(row0 + row) * p.ts.a_row];
+        }
+    }
     typedef std::conditional_t<C::I8, int, float> Sum;
     typedef std::conditional_t<C::I8, i32x4, f32x4> Sums;
     float *const tile = reinterpret_cast<float *>(st);
@@ -146,8 +165,9 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
             *reinterpret_cast<Sums *>(tile + BN * l32 + 4 * ((8 * j + 2 * g + h) ^ (l32 & 7))) =
                 Sums{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
     __syncthreads();
-    for (int e = tid; e < 32 * BN / 2; e += 64 * WAVES) {
-        const int row = e / (BN / 2), col = 2 * (e % (BN / 2));
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+        const int e = tid + u * 64 * WAVES, row = e / (BN / 2), col = 2 * (e % (BN / 2));
         if (row >= t.rows || col >= out_cols) continue;
         const char *from = stages + 4 * (BN * row + 4 * ((col >> 2) ^ (row & 7)) + (col & 3));
         Sum s0 = 0, s1 = 0;
@@ -161,14 +181,8 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
         const bool both = col + 1 < out_cols;
         float v0 = 0.0f, v1 = 0.0f;
         if constexpr (C::I8) {
-            if (owner >= 0) {
-                const float sa = p.ts.a[(int64_t)(row0 + row) * p.ts.a_row];
-                const float *sb = p.ts.b + (int64_t)group * p.ts.b_group + (int64_t)(n0 + col) * p.ts.b_col;
-                const float *bias = p.ts.bias + (int64_t)group * p.ts.bias_group + n0 + col;
-                const bool with = p.ts.bias != nullptr;
-                v0 = int8_value((float)s0, sa, sb[0], with ? bias[0] : 0.0f);
-                if (both) v1 = int8_value((float)s1, sa, sb[p.ts.b_col], with ? bias[1] : 0.0f);
-            }
+            v0 = int8_value((float)s0, row_scale[u], col_scale[0], col_bias[0]);       // (no owner: zeros)
+            v1 = int8_value((float)s1, row_scale[u], col_scale[1], col_bias[1]);
         } else {
             v0 = s0 * p.alpha;
             v1 = s1 * p.alpha;

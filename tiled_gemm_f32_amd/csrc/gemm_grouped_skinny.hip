@@ -189,6 +189,21 @@ grouped_skinny_kernel(GroupedParams p, int tiles_n) {
         __builtin_amdgcn_sched_barrier(0);
     }
 
+    // 8-bit integers: the scales and the bias of this thread's results, under way while the sums are added.  Its
+    // results are all of one column.
+    constexpr int kTurns = (ROWS * COLS + 64 * WAVES - 1) / (64 * WAVES);
+    static_assert(64 * WAVES % COLS == 0, "");
+    float row_scale[kTurns] = {}, col_scale = 0.0f, col_bias = 0.0f;
+    if (DT == kInt8 && owner >= 0 && tid % COLS < cols) {
+        const int col = n0 + tid % COLS;
+        col_scale = p.ts.b[(int64_t)group * p.ts.b_group + (int64_t)col * p.ts.b_col];
+        if (p.ts.bias != nullptr) col_bias = p.ts.bias[(int64_t)group * p.ts.bias_group + col];
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int row = (tid + u * 64 * WAVES) / COLS;
+            if (row < t.rows) row_scale[u] = p.ts.a[(int64_t)(row0 + row) * p.ts.a_row];
+        }
+    }
     __syncthreads();                       // the scales are not needed any more
 #pragma unroll
     for (int q = 0; q < SUMS; ++q)
@@ -199,18 +214,16 @@ grouped_skinny_kernel(GroupedParams p, int tiles_n) {
                 *reinterpret_cast<Acc *>(lds + ((wave + q * WAVES) * ROWS + 16 * i + lc) * COLS + 16 * j + 4 * g) =
                     acc[q][i][j];
     __syncthreads();
-    for (int i = tid; i < ROWS * COLS; i += 64 * WAVES) {
-        const int row = i / COLS, col = i % COLS;
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+        const int i = tid + u * 64 * WAVES, row = i / COLS, col = i % COLS;
         if (row >= t.rows || col >= cols) continue;
         float v = 0.0f;
         if constexpr (DT == kInt8) {
             int sum = 0;
 #pragma unroll
             for (int w = 0; w < kSums; ++w) sum += reinterpret_cast<const int *>(lds)[w * ROWS * COLS + i];
-            if (owner >= 0)
-                v = int8_value((float)sum, p.ts.a[(int64_t)(row0 + row) * p.ts.a_row],
-                               p.ts.b[(int64_t)group * p.ts.b_group + (int64_t)(n0 + col) * p.ts.b_col],
-                               p.ts.bias != nullptr ? p.ts.bias[(int64_t)group * p.ts.bias_group + n0 + col] : 0.0f);
+            v = int8_value((float)sum, row_scale[u], col_scale, col_bias);     // (no owner: zeros)
         } else {
 #pragma unroll
             for (int w = 0; w < kSums; ++w) v += lds[w * ROWS * COLS + i];
