@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -82,8 +83,12 @@ bool out_type(PyObject *o, at::ScalarType otherwise, at::ScalarType &type, int32
     return type == at::kFloat || type == at::kBFloat16 || type == at::kFloat8_e4m3fn;
 }
 
+// (Not through torch's dispatcher, which takes as long as the allocation itself.)
 Tensor make(const Tensor &like, int64_t rows, int64_t cols, int64_t ld, at::ScalarType type) {
-    return at::empty_strided({rows, cols}, {ld, 1}, like.options().dtype(type));
+    return at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.device());
+}
+Tensor row_of(const Tensor &like, int64_t n, at::ScalarType type) {
+    return at::detail::empty_strided_cuda({n}, {1}, type, like.device());
 }
 int64_t blocks(int64_t n) { return (n + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK; }
 int64_t on16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -175,9 +180,9 @@ PyObject *rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const bool with = args[3] != Py_None;
     if (with && (!matrix(args[3], w, type, ds) || ds.rows != dy.rows || ds.cols != dy.cols)) return none();
     const Tensor dx = make(*dy.t, dy.rows, dy.cols, dy.cols, type);
-    const Tensor dweight = at::empty_strided({dy.cols}, {1}, dy.t->options().dtype(at::kFloat));
+    const Tensor dweight = row_of(*dy.t, dy.cols, at::kFloat);
     const int64_t need = gemm_rms_norm_workspace_size(dy.rows, dy.cols);
-    const Tensor space = at::empty_strided({need}, {1}, dy.t->options().dtype(at::kByte));
+    const Tensor space = row_of(*dy.t, need, at::kByte);
     return give(gemm_rms_norm_backward(dtype, dy.rows, dy.cols, dy.data, dy.ld, s.data, s.ld, weight,
                                        (float)PyFloat_AS_DOUBLE(args[4]), with ? ds.data : nullptr, ds.ld,
                                        dx.data_ptr(), dy.cols, static_cast<float *>(dweight.data_ptr()),
@@ -281,16 +286,12 @@ PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
         return none();
     const int64_t groups = tensor(args[2])->size(0), N = dy.cols, K = x.cols;
     if (groups <= 0 || !vector(args[2], w, at::kInt, groups, ends)) return none();
-    const Tensor out = at::empty_strided({groups, N, K}, {N * K, K, 1}, dy.t->options().dtype(at::kFloat));
+    const Tensor out = at::detail::empty_strided_cuda({groups, N, K}, {N * K, K, 1}, at::kFloat, dy.t->device());
     return give(gemm_grouped_wgrad(dtype, (int32_t)groups, static_cast<const int32_t *>(ends), dy.rows, N, K,
                                    (float)PyFloat_AS_DOUBLE(args[3]), dy.data, dy.ld, x.data, x.ld, 0.0f,
                                    static_cast<float *>(out.data_ptr()), K, groups > 1 ? N * K : 0, w.stream),
                 out);
     END_HANDLE_TH_ERRORS
-}
-
-Tensor row_of(const Tensor &like, int64_t n, at::ScalarType type) {
-    return at::empty_strided({n}, {1}, like.options().dtype(type));
 }
 
 // layer_norm(x, weight, bias, residual, eps, out_dtype, device, stream)
