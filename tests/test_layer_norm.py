@@ -179,7 +179,8 @@ def gradients(dy, s, w, ds):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("M,N,pad,offset", SIZES + [(2600, 40, 0, 0), (1600, 1100, 0, 0), (1100, 4100, 0, 0),
+@pytest.mark.parametrize("M,N,pad,offset", SIZES + [(2600, 40, 0, 0), (2200, 1100, 0, 0), (1600, 2100, 0, 0), (1100, 4100, 0, 0),
+                                                    (9, 2048, 0, 0), (3, 2049, 1, 1),
                                                     (1030, 8200, 0, 0)])
 def test_backward(gpu_available, dtype, M, N, pad, offset):
     x, s, w, _ = inputs(M, N, dtype)

@@ -414,16 +414,19 @@ template <int DT, bool LARGE> hipError_t norm_type(const LayerNormParams &p, hip
 // Workgroups of the backward pass: enough to fill the compute units with teams that each still take several
 // rows, so that the partial sums stay a small part of what is moved.
 int grad_workgroups(int64_t M, int64_t N) {
-    const int64_t rows = N <= 1024 ? (M + 3) / 4 : M;        // rows a workgroup takes at once: 4, or 1
+    const int64_t rows = N <= 2048 ? (M + 3) / 4 : M;        // rows a workgroup takes at once: 4, or 1
     return (int)(rows < 512 ? rows : 512);
 }
 
-// (8192 x 8192 bf16 in 1024 threads and one chunk 114 us, in 512 and two 102.)
+// Here more chunks a lane pay, as a row's two trips around the team cost more than its loads.  8192 rows bf16 of 2048
+// in 64 threads and four chunks 28 us, in 256 and two 40; of 8192 in 256 and four 96, in 512 and two 101, in 1024 and
+// one 115; 5366 x 8176 fp32 150, 154 and 164.
 template <int DT, bool LARGE> hipError_t grad_type(const LayerNormGradParams &p, hipStream_t s) {
     const dim3 grid((unsigned)grad_workgroups(p.M, p.N));
     if (p.N <= 1024) return go(&layer_norm_backward_kernel<DT, 64, 2, LARGE>, grid, 256, s, p);
+    if (p.N <= 2048) return go(&layer_norm_backward_kernel<DT, 64, 4, LARGE>, grid, 256, s, p);
     if (p.N <= 4096) return go(&layer_norm_backward_kernel<DT, 256, 2, LARGE>, grid, 256, s, p);
-    if (p.N <= 8192) return go(&layer_norm_backward_kernel<DT, 512, 2, LARGE>, grid, 512, s, p);
+    if (p.N <= 8192) return go(&layer_norm_backward_kernel<DT, 256, 4, LARGE>, grid, 256, s, p);
     if (p.N <= 16384) return go(&layer_norm_backward_kernel<DT, 512, 4, LARGE>, grid, 512, s, p);
     return go(&layer_norm_backward_long_kernel<DT>, grid, 1024, s, p);
 }

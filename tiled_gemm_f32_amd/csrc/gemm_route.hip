@@ -386,11 +386,11 @@ template <int DT, bool LARGE> hipError_t combine_grad_type(const CombineGradPara
 
 }  // namespace
 
-// One workgroup for few choices: a second launch costs as much as four steps of its waves (2048 choices of 64
-// groups 6.2 us in one, 6.8 in five; 8192 of 128 groups 14.0 and 8.2).  Each of several then adds up the counts
-// of all, which bounds how many pay (65536 of 64: 8.4 us in 64, 7.9 in 128; 524288: 18.2 and 13.4).
+// One workgroup for few choices: a second launch costs the GPU as much as five steps of its waves (2400 choices of
+// 64 groups 7.05 us in one workgroup, 6.95 in five; 8192 of 128 groups 14.0 and 8.2).  Each of several then adds up
+// the counts of all, which bounds how many pay (65536 of 64: 8.4 us in 64, 7.9 in 128; 524288: 18.2 and 13.4).
 int plan_blocks(int64_t choices) {
-    return choices <= 2048 ? 1 : (int)std::min((choices + 511) / 512, (int64_t)128);
+    return choices <= 2560 ? 1 : (int)std::min((choices + 511) / 512, (int64_t)128);
 }
 
 hipError_t launch_plan(const PlanParams &p, hipStream_t s) {
