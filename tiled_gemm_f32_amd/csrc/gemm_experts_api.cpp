@@ -387,9 +387,6 @@ GEMM_API gemm_status gemm_int8(int32_t op_b, int32_t groups, const int32_t *ends
         return launched(gemm::launch_int8_general(op_b, p, s));
     if (M == 1) p.lda = ceil_div(K, 16) * 16;                        // the stride of a single row is not used
     const bool dma = rows_on16(A, p.lda, 1) && rows_on16(B, ldb, 1) && stride_b % 16 == 0;
-    if (dma)
-        if (const int rows = gemm::skinny_rows(gemm::kInt8, op_b, p))
-            return launched(gemm::launch_grouped_skinny(gemm::kInt8, rows, p, s));
     return launched(gemm::launch_grouped_int8(op_b, dma, p, s));
 }
 

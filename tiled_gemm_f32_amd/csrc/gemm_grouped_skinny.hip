@@ -23,14 +23,11 @@
 // fp8 with block scales: a block is one scale block.  Its partial sums are
 // multiplied by a(row) * b(column block) as they are added; the products of
 // the two scales are made once a workgroup, in LDS, under the first loads.
-#include <type_traits>
-
 #include "gemm_grouped.hpp"
 
 namespace gemm {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSums = 8;                  // partial sums of a result: blocks b with equal b % 8
@@ -57,17 +54,6 @@ template <> struct Skinny<GEMM_DTYPE_BF16F32> {
         for (int h = 0; h < 2; ++h)
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[h]),
                                                           __builtin_bit_cast(bf16x8, a[h]), acc, 0, 0, 0);
-        return acc;
-    }
-};
-
-template <> struct Skinny<kInt8> {
-    static constexpr int esz = 1;
-    static __device__ __forceinline__ i32x4 mma(const u32x4 (&w)[2], const u32x4 (&a)[2], i32x4 acc) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[h]), __builtin_bit_cast(i32x4, a[h]),
-                                                        acc, 0, 0, 0);
         return acc;
     }
 };
@@ -136,8 +122,7 @@ grouped_skinny_kernel(GroupedParams p, int tiles_n) {
         __syncthreads();
     }
 
-    typedef std::conditional_t<DT == kInt8, i32x4, f32x4> Acc;
-    Acc acc[SUMS][MT][CG] = {};
+    f32x4 acc[SUMS][MT][CG] = {};
     // Weights as the first operand, A as the second: register r of lane (g,
     // lc) is column 4g + r of the 16, row lc.
     auto consume = [&](int set, int first) __attribute__((always_inline)) {
@@ -189,21 +174,6 @@ grouped_skinny_kernel(GroupedParams p, int tiles_n) {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // 8-bit integers: the scales and the bias of this thread's results, under way while the sums are added.  Its
-    // results are all of one column.
-    constexpr int kTurns = (ROWS * COLS + 64 * WAVES - 1) / (64 * WAVES);
-    static_assert(64 * WAVES % COLS == 0, "");
-    float row_scale[kTurns] = {}, col_scale = 0.0f, col_bias = 0.0f;
-    if (DT == kInt8 && owner >= 0 && tid % COLS < cols) {
-        const int col = n0 + tid % COLS;
-        col_scale = p.ts.b[(int64_t)group * p.ts.b_group + (int64_t)col * p.ts.b_col];
-        if (p.ts.bias != nullptr) col_bias = p.ts.bias[(int64_t)group * p.ts.bias_group + col];
-#pragma unroll
-        for (int u = 0; u < kTurns; ++u) {
-            const int row = (tid + u * 64 * WAVES) / COLS;
-            if (row < t.rows) row_scale[u] = p.ts.a[(int64_t)(row0 + row) * p.ts.a_row];
-        }
-    }
     __syncthreads();                       // the scales are not needed any more
 #pragma unroll
     for (int q = 0; q < SUMS; ++q)
@@ -211,24 +181,16 @@ grouped_skinny_kernel(GroupedParams p, int tiles_n) {
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < CG; ++j)
-                *reinterpret_cast<Acc *>(lds + ((wave + q * WAVES) * ROWS + 16 * i + lc) * COLS + 16 * j + 4 * g) =
+                *reinterpret_cast<f32x4 *>(lds + ((wave + q * WAVES) * ROWS + 16 * i + lc) * COLS + 16 * j + 4 * g) =
                     acc[q][i][j];
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kTurns; ++u) {
-        const int i = tid + u * 64 * WAVES, row = i / COLS, col = i % COLS;
+    for (int i = tid; i < ROWS * COLS; i += 64 * WAVES) {
+        const int row = i / COLS, col = i % COLS;
         if (row >= t.rows || col >= cols) continue;
         float v = 0.0f;
-        if constexpr (DT == kInt8) {
-            int sum = 0;
 #pragma unroll
-            for (int w = 0; w < kSums; ++w) sum += reinterpret_cast<const int *>(lds)[w * ROWS * COLS + i];
-            v = int8_value((float)sum, row_scale[u], col_scale, col_bias);     // (no owner: zeros)
-        } else {
-#pragma unroll
-            for (int w = 0; w < kSums; ++w) v += lds[w * ROWS * COLS + i];
-            v *= p.alpha;
-        }
+        for (int w = 0; w < kSums; ++w) v += lds[w * ROWS * COLS + i];
+        v *= p.alpha;
         const int64_t at = (int64_t)(row0 + row) * p.ldo + n0 + col;
         if (p.out_type == GEMM_OUT_BF16) static_cast<uint16_t *>(p.out)[at] = to_bf16(v);
         else static_cast<float *>(p.out)[at] = v;
@@ -277,7 +239,6 @@ int skinny_rows(int32_t dtype, int32_t op_b, const GroupedParams &p) {
 }
 
 hipError_t launch_grouped_skinny(int32_t dtype, int rows, const GroupedParams &p, hipStream_t stream) {
-    if (dtype == kInt8) return launch_rows<kInt8>(rows, p, stream);
     return dtype == GEMM_DTYPE_FP8F32 ? launch_rows<GEMM_DTYPE_FP8F32>(rows, p, stream)
                                       : launch_rows<GEMM_DTYPE_BF16F32>(rows, p, stream);
 }

@@ -885,6 +885,19 @@ inline double deep_time(double rows, double cols, double slabs, double groups, i
     return (bn == 32 ? std::max(1.0, turns) : std::ceil(turns)) * (std::ceil(slabs / 8) * each + 4.0) + 2.5;
 }
 
+// The same for 8-bit integers and weights stored N x K, in tiles of 32 x 32: rounds of eight slabs, and 512 workgroups
+// at a time.  Inputs changing from call to call, us: 512 x 1024 x 1024 5.4, and 6.1 in 32 x 128; 128 x 4096 x 4096
+// 10.5 and 12; 64 x 8192 x 8192 17.4 and 19; but 256 x 4096 x 4096 16.1 and 12.0.  Few rows against long ones of many
+// weights are bound by how many loads are under way, and always go here: 64 rows over 32 groups of 4096 x 4096 82 us
+// (5.3 TB/s), 107 to 121 in the tiles; 16 x 16384 x 8192 27 and 36.
+inline double deep_time_int8(double rows, double cols, double slabs, double groups, bool dma) {
+    if (dma && rows <= 32 * groups && slabs >= 32) return 0.0;
+    const double high = groups > 1 ? 1.1 * groups * std::max(1.0, rows / groups / 32 + 0.5) : std::ceil(rows / 32);
+    const double turns = high * std::ceil(cols / 32) / 512, rounds = std::ceil(slabs / 8);
+    return dma ? std::max(0.55 * rounds + 0.6, turns * (1.17 * rounds + 1.35)) + 5.4
+               : std::max(1.3 * rounds, turns * (2.5 * rounds + 1.45)) + 3.8;
+}
+
 // 16 instructions of 64 cycles for each of 4 x 4 fragment pairs, on four matrix cores.
 constexpr double kMatrixF32 = 1.75;
 
@@ -898,8 +911,9 @@ template <int DT, bool BKN, bool DMA> hipError_t launch_sized(const GroupedParam
     constexpr TileSize first = F32 ? kTile128 : DMA ? kTile256 : FP8 ? kTile64 : kTile192;
     const TileChoice c = tile_choice(p.M, p.N, slabs, groups, first, F32 ? kMatrixF32 : 0.0, DMA ? 0.0 : 0.15);
     constexpr int32_t op = BKN ? GEMM_OP_N : GEMM_OP_T;
-    if (deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6) < c.time &&
-        deep_takes(DT, op, DMA, p))
+    const double deep = I8 ? deep_time_int8(p.M, p.N, slabs, groups, DMA)
+                           : deep_time(p.M, p.N, slabs, groups, deep_columns(DT, BKN), F32 || BKN || !DMA ? 0.9 : 0.6);
+    if (deep < c.time && deep_takes(DT, op, DMA, p))
         return launch_grouped_deep(DT, op, DMA, p, s);
     switch (c.size) {
         case kTile256:
