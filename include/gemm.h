@@ -643,7 +643,7 @@ GEMM_API gemm_status gemm_layer_norm_backward(int32_t dtype, int64_t M, int64_t 
  * in fp32, to the nearest integer with ties to even: -127 .. 127.  A row that
  * holds an infinity or a NaN has codes of 0 and a scale of NaN, so that the
  * products made of it are NaN.  Row i of Q starts at Q + i*ldq; scales has M
- * values.
+ * values.  K == 0 writes nothing.
  */
 GEMM_API gemm_status gemm_quantize_int8(int32_t dtype, int64_t M, int64_t K, const void *X, int64_t ldx,
                                         int8_t *Q, int64_t ldq, float *scales, gemm_stream_t stream);
@@ -717,7 +717,7 @@ GEMM_API gemm_status gemm_expert_plan(int32_t id_bytes, int64_t tokens, int32_t 
  * were.  A place outside 0 .. rows-1 (or from *last on) is taken as none;
  * places must be distinct.  scale_cols > 0 moves as many floats a token
  * along, from scales (row t at t*lds) to out_scales (row i at i*ldos): the
- * scales of quantised rows.  out overlaps no input.
+ * scales of quantised rows.  N == 0 writes nothing.  out overlaps no input.
  */
 GEMM_API gemm_status gemm_dispatch(int32_t elem_bytes, int64_t tokens, int32_t top, int64_t N, const void *X,
                                    int64_t ldx, const int32_t *place, const int32_t *last, int64_t rows, void *out,

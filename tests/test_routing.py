@@ -147,7 +147,7 @@ def of_choices(rows, place):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("cols", COLS)
 def test_combine(gpu_available, dtype, cols):
-    for tokens, top, groups, pad, offset in ((1, 1, 1, 0, 0), (37, 3, 5, 3, 1), (130, 9, 16, 8, 0)):
+    for tokens, top, groups, pad, offset in ((1, 1, 1, 0, 0), (37, 3, 5, 3, 1), (130, 9, 16, 8, 0), (7, 131, 16, 0, 0)):
         _, place, ends = tg.expert_plan(case(tokens, top, groups), groups)
         g = gen(cols + tokens)
         rows = torch.randn(tokens * top, cols, generator=g).to(dtype)

@@ -21,6 +21,9 @@
 // N, 21 of them with rows, 72 us (4.9 TB/s); 64 x 1000 x 1024 fp32 7.8 us, 3.5 of
 // them matrix instructions.
 //
+// 8-bit integers: 16 x 8192 x 8192 12.3 us (67 MB of weights, 5.4 TB/s), 64 rows over 32 experts of 4096 x 4096, 26
+// of them with rows, 78 us (5.6 TB/s).
+//
 // Loads, layouts and fragments are those of gemm_grouped_tile.hpp with one
 // wave.  fp8: the products of the two block scales are made once a workgroup,
 // in LDS, under the first loads.

@@ -23,6 +23,10 @@
 // 0.87 busy (a slab of 128 x 128 takes 1.75 us of them, 0.6 of loads; 8 uneven
 // groups of 8192 x 2048 x 1024 285 us, 121 TF; 8192 x 4096 x 4096 1.88 ms, 146).
 //
+// 8-bit integers (32-bit accumulators, scaled in the epilogue): 8192^3 437 to 461 us, 2.4 to 2.5 P operations a
+// second (a library's product 454), the matrix cores 0.72 busy; 2048 x 4096 x 4096 37 us, 0.57 busy; 8192 rows in 16
+// uneven groups of 4096 x 4096 170 to 184 us, 0.48 busy, of even groups 140, of one 125.
+//
 // fp8 with block scales: the matrix core sums a block of 128 k into a partial
 // tile of its own (two v_mfma_f32_32x32x64_f8f6f4, the first with a zero
 // addend), which is then added to the accumulators times the block's scale,

@@ -7,13 +7,18 @@
 // is large beside its deviation.  y = (s - mean) * r * weight + bias.  Codes with a scale a row take a third
 // trip, for the row's largest magnitude.  Rows past 16384 values are walked once for each of these, from the
 // caches after the first.
+//
+// Measured (a copy reaches 5.2 TB/s here): 8192 x 4096 bf16 in training, 268 MB each way, forward 47 us (5.7 TB/s),
+// backward 50 (5.3) and 5 for the last sum over partial rows; 8192 x 8192 bf16 with a residual to codes with a scale a
+// row, 470 MB, 86 to 91 us (5.2 to 5.5); 5366 x 8176 fp32 135 and 150 us (5.2 and 4.7).  1000 x 777 fp32: 6.7, 6.3
+// and 3.3 us, a launch each and two trips around a wave.  Codes of 8192 x 4096 bf16 18 us (5.6 TB/s).
 #include "gemm_norm.hpp"
 #include "gemm_rows.hpp"
 
 namespace gemm {
 namespace {
 
-// y of one chunk out, or nothing yet (codes with a scale a row).
+// A chunk's codes with a scale a row out.
 __device__ __forceinline__ void put_codes(const LayerNormParams &p, int64_t row, int64_t col, f32x8 y, int n,
                                           uint32_t top, float inv) {
     store_codes(static_cast<uint8_t *>(p.out) + row * p.ldo + col, row_codes8(y, top, inv), n);

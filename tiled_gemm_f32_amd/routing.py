@@ -75,6 +75,7 @@ def expert_plan(experts, groups: int, stream=None):
     device = _device(experts, "experts")
     _check(experts, "experts", device)
     tokens, top = experts.shape
+    groups = int(groups)
     if top < 1 or groups < 1:
         raise ValueError(f"a token has one choice at least, of one group at least (got {top}, {groups})")
 
