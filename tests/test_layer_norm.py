@@ -206,6 +206,32 @@ def test_backward(gpu_available, dtype, M, N, pad, offset):
     assert none[1] is None and none[2] is None and torch.equal(none[0], got[0]) and none[0] is args[0]
 
 
+# Operands of 32 MB and more, in every shape of a row: passes that go past the L2.
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [1000, 1024, 2048, 4000, 8192, 16384])
+def test_large_passes(gpu_available, dtype, N):
+    M = 2 ** 25 // (4 if dtype == F32 else 2) // N + 70
+    say(f"[layer norm] large {dtype} {M}x{N}")
+    x, res, w, b = inputs(M, N, dtype)
+    xd, rd, wd, bd = x.cuda(), res.cuda(), w.cuda(), b.cuda()
+    s = (x.float() + res.float()).to(dtype)
+    y, tol = reference(s, w, b)
+    out, summed, _ = tg.layer_norm(xd, wd, bd, residual=rd, eps=EPS)
+    assert torch.equal(summed.cpu(), s)
+    within(out, y, tol + HALF[dtype] * (y.abs() + tol), "y")
+    codes, summed, scales = tg.layer_norm(xd, wd, bd, residual=rd, eps=EPS, out_dtype=I8)
+    assert torch.equal(summed.cpu(), s)
+    step = f64(scales)[:, None]
+    within(f64(codes) * step, y, 0.5 * step * (1 + 2.0 ** -10) + tol + 4 * U32 * y.abs(), "int8 values")
+    want, off = gradients(x, s, w, res)
+    got = tg.layer_norm_backward(xd, summed, wd, dsum=rd, eps=EPS)
+    # a team takes M / 512 rows and more, one after the other
+    more = 1 + M / 512 / 96
+    within(got[0], want[0], off[0] + HALF[dtype] * (want[0].abs() + off[0]), "dx")
+    within(got[1], want[1], off[1] * more, "dw")
+    within(got[2], want[2], off[2] * more, "db")
+
+
 def test_gradients_against_differences(gpu_available):
     M, N, h = 4, 37, 1e-2
     x, _, w, b = (t.double() for t in inputs(M, N, F32))

@@ -204,6 +204,31 @@ def test_combine_backward(gpu_available, dtype, cols):
         assert again is args[1] and torch.equal(again, drows) and torch.equal(dw, dweights)
 
 
+# Rows of 32 MB and more in all, which go past the L2, and of less in as many waves.
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,top,cols", [(5000, 1, 1000), (9000, 2, 1000), (2500, 2, 4000), (1300, 2, 8000), (700, 3, 16400)])
+def test_many_rows(gpu_available, dtype, tokens, top, cols):
+    say(f"[routing] many rows {dtype} {tokens} x {top} x {cols}")
+    order, place, ends = tg.expert_plan(case(tokens, top, 20, 0.1), 20)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x, d = (torch.randn(tokens, cols, device="cuda", generator=g).to(dtype) for _ in range(2))
+    w = torch.rand(tokens, top, device="cuda", generator=g)
+    rows = tg.dispatch(x, place, ends)
+    token, have = order.clamp_min(0).long() // top, (order >= 0)[:, None]
+    assert torch.equal(rows, torch.where(have, x[token], torch.zeros((), dtype=dtype, device="cuda")))
+    each = torch.where((place >= 0)[:, :, None], rows[place.clamp_min(0).long()].double(), torch.zeros((), device="cuda").double())
+    terms = each * w.double()[:, :, None]
+    want = d.double() + terms.sum(dim=1)
+    tol = (top + 1) * U32 * (d.double().abs() + terms.abs().sum(dim=1)) * (1 + U16)
+    got = tg.combine(rows, place, w, d)
+    assert ((got.double() - want).abs() <= tol + HALF[dtype] * (want.abs() + tol)).all()
+    drows, dw = tg.combine_backward(d, rows, place, w, ends)
+    value = torch.where(have, w.flatten()[order.clamp_min(0).long()].double()[:, None] * d[token].double(), 0.0)
+    assert ((drows.double() - value).abs() <= (U32 + HALF[dtype] * (1 + U16)) * value.abs() * (1 + U16) + 1e-45).all()
+    products = each * d.double()[:, None, :]
+    assert ((dw.double() - products.sum(dim=2)).abs() <= depth(cols) * U32 * products.abs().sum(dim=2) * (1 + U16)).all()
+
+
 def test_gradients_against_differences(gpu_available):
     """combine(f(dispatch(x))) with f one weight a row, its gradients through the operators against differences."""
     tokens, top, groups, cols, h = 6, 3, 4, 20, 0.25
