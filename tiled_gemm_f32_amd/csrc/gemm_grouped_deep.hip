@@ -144,7 +144,6 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     for (int i = 0; i + 1 < mine; ++i) step(i, false);
     if (mine > 0) step(mine - 1, true);
 
-    // Partial tiles: row l32 of 8 * FN chunks of 4 columns, chunk c at c ^ (row & 7).
     // 8-bit integers: the scales and the bias of this thread's results, under way while the sums are added.  Its
     // results are all of two columns.
     constexpr int kTurns = (32 * BN / 2 + 64 * WAVES - 1) / (64 * WAVES);
@@ -166,6 +165,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
     }
     typedef std::conditional_t<C::I8, int, float> Sum;
     typedef std::conditional_t<C::I8, i32x4, f32x4> Sums;
+    // Partial tiles: row l32 of 8 * FN chunks of 4 columns, chunk c at c ^ (row & 7).
     float *const tile = reinterpret_cast<float *>(st);
 #pragma unroll
     for (int j = 0; j < FN; ++j)

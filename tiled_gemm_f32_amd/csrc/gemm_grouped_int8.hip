@@ -1,10 +1,10 @@
 // Products of 8-bit integers with a scale for each token and channel: the tiles of gemm_grouped_tile.hpp with
-// 32-bit accumulators, and a general kernel, for the calls that those do not take: a row
-// of an operand is shorter than one 16-byte load, or rows lie so far apart that a tile's panel passes the 2 GiB a buffer load can address.  Every
-// layout, stride and alignment is right here.  An output tile of 64 x 64, 64 k of both operands staged a
-// byte at a time through registers into LDS as [row][k], four waves each keeping a quarter of the tile in 32-bit
-// accumulators, two v_mfma_i32_32x32x32_i8 a slab.  Such calls are bound by their results' stores, or by one
-// memory transaction a row.
+// 32-bit accumulators, and a general kernel for the calls that those do not take, where a row of an operand is
+// shorter than one 16-byte load, or rows lie so far apart that a tile's panel passes the 2 GiB a buffer load can
+// address.  Every layout, stride and alignment is right here.  An output tile of 64 x 64, 64 k of both operands
+// staged a byte at a time through registers into LDS as [row][k], four waves each keeping a quarter of the tile
+// in 32-bit accumulators, two v_mfma_i32_32x32x32_i8 a slab.  Such calls are bound by their results' stores, or
+// by one memory transaction a row.
 #include "gemm_grouped_tile.hpp"
 
 namespace gemm {
