@@ -118,7 +118,7 @@ grouped_deep_kernel(GroupedParams p, int tiles_n) {
         }
         if ((last || C::I8) && (!C::DMA || len % C::BK != 0) && slab == slabs - 1) {
             a.cut(slab, st, lane);
-            b.cut(slab, st + C::kA, lane);
+            if (!C::I8 || !C::DMA) b.cut(slab, st + C::kA, lane);       // (integers: A's zeros do)
         }
         const FragOf<C::esz> fa = read_frag<C, false>(st, a_base, 0);
         FragOf<C::esz> fb[FN];
