@@ -718,6 +718,8 @@ GEMM_API gemm_status gemm_expert_plan(int32_t id_bytes, int64_t tokens, int32_t 
  * places must be distinct.  scale_cols > 0 moves as many floats a token
  * along, from scales (row t at t*lds) to out_scales (row i at i*ldos): the
  * scales of quantised rows.  N == 0 writes nothing.  out overlaps no input.
+ * Here and in the two calls below, top and scale_cols are at most 2^31 - 64
+ * (GEMM_ERR_UNSUPPORTED past that).
  */
 GEMM_API gemm_status gemm_dispatch(int32_t elem_bytes, int64_t tokens, int32_t top, int64_t N, const void *X,
                                    int64_t ldx, const int32_t *place, const int32_t *last, int64_t rows, void *out,

@@ -16,8 +16,12 @@ bool bad_opt(const void *p, uintptr_t esz) { return p != nullptr && bad_ptr(p, e
 bool float_type(int32_t dtype) { return dtype == GEMM_DTYPE_F32 || dtype == GEMM_DTYPE_BF16F32; }
 uintptr_t size_of(int32_t dtype) { return dtype == GEMM_DTYPE_F32 ? 4 : 2; }
 bool past(int64_t a, int64_t b, int64_t c, int64_t d) { return a > kMaxDim || b > kMaxDim || c > kMaxDim || d > kMaxDim; }
+// A token's choices and its scales are walked 64 at a time in 32-bit numbers, which go that far past the last one.
+constexpr int64_t kMostWalked = kMaxDim - 63;
 // Choices of a call are numbered in 32 bits.
-bool many_choices(int64_t tokens, int32_t top) { return tokens > kMaxDim || (top > 0 && tokens > kMaxDim / top); }
+bool many_choices(int64_t tokens, int32_t top) {
+    return tokens > kMaxDim || top > kMostWalked || (top > 0 && tokens > kMaxDim / top);
+}
 
 gemm_status launched(hipError_t err) { return err == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
@@ -74,7 +78,8 @@ GEMM_API gemm_status gemm_dispatch(int32_t elem_bytes, int64_t tokens, int32_t t
     if (rows > 0 && N > 0 &&
         (bad_ptr(out, (uintptr_t)elem_bytes) || bad_opt(last, 4) || (scale_cols > 0 && bad_ptr(out_scales, 4))))
         return GEMM_ERR_INVALID_ARG;
-    if (many_choices(tokens, top) || past(N, ldx, ldo, rows) || (scale_cols > 0 && past(scale_cols, lds, ldos, 0)))
+    if (many_choices(tokens, top) || past(N, ldx, ldo, rows) || scale_cols > kMostWalked ||
+        (scale_cols > 0 && past(0, lds, ldos, 0)))
         return GEMM_ERR_UNSUPPORTED;
     if (rows == 0 || N == 0 || (tokens == 0 && last == nullptr)) return GEMM_OK;
     gemm_status st = gemm::check_device();
