@@ -365,16 +365,25 @@ def gemm_block_scaled(op_b, M, N, K, alpha, A, lda, B, ldb, scales, out_type, ou
     return load().gemm_block_scaled(op_b, M, N, K, alpha, A, lda, B, ldb, scales, out_type, out, ldo, stream)
 
 
+def _not_32_bit(*counts) -> int:
+    """The status of a call with a count that its 32-bit argument cannot hold, or 0: ctypes would pass on the
+    count's lower bits, which may be a valid one."""
+    for n in counts:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            return GEMM_ERR_UNSUPPORTED if n > 0 else GEMM_ERR_INVALID_ARG
+    return GEMM_OK
+
+
 def gemm_grouped(dtype, op_b, groups, ends, M, N, K, alpha, A, lda, B, ldb, stride_b, scales, out_type, out, ldo,
                  stream=0) -> int:
-    return load().gemm_grouped(dtype, op_b, groups, ends, M, N, K, alpha, A, lda, B, ldb, stride_b, scales, out_type,
-                               out, ldo, stream)
+    return _not_32_bit(groups) or load().gemm_grouped(
+        dtype, op_b, groups, ends, M, N, K, alpha, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream)
 
 
 def gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w,
                        stream=0) -> int:
-    return load().gemm_grouped_wgrad(dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w,
-                                     stream)
+    return _not_32_bit(groups) or load().gemm_grouped_wgrad(
+        dtype, groups, ends, M, N, K, alpha, dY, lddy, X, ldx, beta, dW, ldw, stride_w, stream)
 
 
 def gemm_layer_norm(dtype, M, N, X, ldx, residual, ldr, weight, bias, eps, sum, ld_sum, out_type, out, ldo, scales=0,
@@ -398,32 +407,35 @@ def gemm_quantize_int8(dtype, M, K, X, ldx, Q, ldq, scales, stream=0) -> int:
 
 
 def gemm_int8(op_b, groups, ends, M, N, K, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream=0) -> int:
-    return load().gemm_int8(op_b, groups, ends, M, N, K, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream)
+    return _not_32_bit(groups) or load().gemm_int8(
+        op_b, groups, ends, M, N, K, A, lda, B, ldb, stride_b, scales, out_type, out, ldo, stream)
 
 
 def gemm_expert_plan_workspace_size(tokens, top, groups) -> int:
-    return int(load().gemm_expert_plan_workspace_size(tokens, top, groups))
+    return 0 if _not_32_bit(top, groups) else int(load().gemm_expert_plan_workspace_size(tokens, top, groups))
 
 
 def gemm_expert_plan(id_bytes, tokens, top, groups, experts, ld, order, place, ends, workspace=0, workspace_bytes=0,
                      stream=0) -> int:
-    return load().gemm_expert_plan(id_bytes, tokens, top, groups, experts, ld, order, place, ends, workspace,
-                                   workspace_bytes, stream)
+    return _not_32_bit(top, groups) or load().gemm_expert_plan(
+        id_bytes, tokens, top, groups, experts, ld, order, place, ends, workspace, workspace_bytes, stream)
 
 
 def gemm_dispatch(elem_bytes, tokens, top, N, X, ldx, place, last, rows, out, ldo, scale_cols=0, scales=0, lds=0,
                   out_scales=0, ldos=0, stream=0) -> int:
-    return load().gemm_dispatch(elem_bytes, tokens, top, N, X, ldx, place, last, rows, out, ldo, scale_cols, scales,
-                                lds, out_scales, ldos, stream)
+    return _not_32_bit(top) or load().gemm_dispatch(
+        elem_bytes, tokens, top, N, X, ldx, place, last, rows, out, ldo, scale_cols, scales, lds, out_scales, ldos,
+        stream)
 
 
 def gemm_combine(dtype, tokens, top, N, rows, ldr, n_rows, place, weights, ldw, residual, ld_res, out, ldo,
                  stream=0) -> int:
-    return load().gemm_combine(dtype, tokens, top, N, rows, ldr, n_rows, place, weights, ldw, residual, ld_res, out,
-                               ldo, stream)
+    return _not_32_bit(top) or load().gemm_combine(
+        dtype, tokens, top, N, rows, ldr, n_rows, place, weights, ldw, residual, ld_res, out, ldo, stream)
 
 
 def gemm_combine_backward(dtype, tokens, top, N, dout, lddo, rows, ldr, n_rows, place, last, weights, ldw, drows, lddr,
                           dweights=0, lddw=0, stream=0) -> int:
-    return load().gemm_combine_backward(dtype, tokens, top, N, dout, lddo, rows, ldr, n_rows, place, last, weights,
-                                        ldw, drows, lddr, dweights, lddw, stream)
+    return _not_32_bit(top) or load().gemm_combine_backward(
+        dtype, tokens, top, N, dout, lddo, rows, ldr, n_rows, place, last, weights, ldw, drows, lddr, dweights, lddw,
+        stream)

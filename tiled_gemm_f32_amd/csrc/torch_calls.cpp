@@ -21,6 +21,9 @@ namespace {
 
 using at::Tensor;
 
+// Groups that the C entry points' 32-bit numbers hold.
+constexpr int64_t kMostGroups = 0x7fffffff;
+
 // A matrix (or, of three dimensions, a stack of them) with unit stride along its rows.
 struct Matrix {
     const Tensor *t = nullptr;
@@ -50,6 +53,7 @@ bool matrix(PyObject *o, const Where &w, at::ScalarType type, Matrix &m, int dim
         m.stride = m.groups > 1 ? strides[0] : 0;
     }
     if (m.groups <= 0 || m.rows <= 0 || m.cols <= 0 || (m.cols > 1 && strides[dim - 1] != 1)) return false;
+    if (m.groups > kMostGroups) return false;
     m.ld = m.rows > 1 ? strides[dim - 2] : m.cols;
     if (m.ld < m.cols) return false;
     m.data = m.t->data_ptr();
@@ -285,7 +289,7 @@ PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
         tensor(args[2])->dim() != 1 || !PyFloat_Check(args[3]))
         return none();
     const int64_t groups = tensor(args[2])->size(0), N = dy.cols, K = x.cols;
-    if (groups <= 0 || !vector(args[2], w, at::kInt, groups, ends)) return none();
+    if (groups <= 0 || groups > kMostGroups || !vector(args[2], w, at::kInt, groups, ends)) return none();
     const Tensor out = at::detail::empty_strided_cuda({groups, N, K}, {N * K, K, 1}, at::kFloat, dy.t->device());
     return give(gemm_grouped_wgrad(dtype, (int32_t)groups, static_cast<const int32_t *>(ends), dy.rows, N, K,
                                    (float)PyFloat_AS_DOUBLE(args[3]), dy.data, dy.ld, x.data, x.ld, 0.0f,
