@@ -11,6 +11,9 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -87,13 +90,26 @@ bool out_type(PyObject *o, at::ScalarType otherwise, at::ScalarType &type, int32
     return type == at::kFloat || type == at::kBFloat16 || type == at::kFloat8_e4m3fn;
 }
 
-// (Not through torch's dispatcher, which takes as long as the allocation itself.)
+// Whether anything but the allocation would see or change an allocation that goes through torch's dispatcher:
+// a dispatch mode or another key that this thread's state adds (functional transforms, tracing), a profiler's
+// callbacks, or the filling of uninitialised memory in deterministic mode.
+bool watched() {
+    const auto &global = at::globalContext();
+    return c10::impl::TorchDispatchModeTLS::any_modes_set() ||
+           !(c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() ||
+           at::hasCallbacks() ||
+           (global.deterministicAlgorithms() && global.deterministicFillUninitializedMemory());
+}
+
+// The dispatcher takes as long as the allocation itself (0.3 us a result), so it is passed by where nobody watches.
+Tensor allocate(const Tensor &like, at::IntArrayRef sizes, at::IntArrayRef strides, at::ScalarType type) {
+    if (watched()) return at::empty_strided(sizes, strides, like.options().dtype(type));
+    return at::detail::empty_strided_cuda(sizes, strides, type, like.device());
+}
 Tensor make(const Tensor &like, int64_t rows, int64_t cols, int64_t ld, at::ScalarType type) {
-    return at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.device());
+    return allocate(like, {rows, cols}, {ld, 1}, type);
 }
-Tensor row_of(const Tensor &like, int64_t n, at::ScalarType type) {
-    return at::detail::empty_strided_cuda({n}, {1}, type, like.device());
-}
+Tensor row_of(const Tensor &like, int64_t n, at::ScalarType type) { return allocate(like, {n}, {1}, type); }
 int64_t blocks(int64_t n) { return (n + GEMM_SCALE_BLOCK - 1) / GEMM_SCALE_BLOCK; }
 int64_t on16(int64_t n) { return (n + 15) / 16 * 16; }
 
@@ -290,7 +306,7 @@ PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
         return none();
     const int64_t groups = tensor(args[2])->size(0), N = dy.cols, K = x.cols;
     if (groups <= 0 || groups > kMostGroups || !vector(args[2], w, at::kInt, groups, ends)) return none();
-    const Tensor out = at::detail::empty_strided_cuda({groups, N, K}, {N * K, K, 1}, at::kFloat, dy.t->device());
+    const Tensor out = allocate(*dy.t, {groups, N, K}, {N * K, K, 1}, at::kFloat);
     return give(gemm_grouped_wgrad(dtype, (int32_t)groups, static_cast<const int32_t *>(ends), dy.rows, N, K,
                                    (float)PyFloat_AS_DOUBLE(args[3]), dy.data, dy.ld, x.data, x.ld, 0.0f,
                                    static_cast<float *>(out.data_ptr()), K, groups > 1 ? N * K : 0, w.stream),
