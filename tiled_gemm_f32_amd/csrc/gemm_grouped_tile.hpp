@@ -913,8 +913,9 @@ inline double deep_time(double rows, double cols, double slabs, double groups, i
 // The same for 8-bit integers and weights stored N x K, in tiles of 32 x 32: rounds of eight slabs, and 512 workgroups
 // at a time.  Inputs changing from call to call, us: 512 x 1024 x 1024 5.4, and 6.1 in 32 x 128; 128 x 4096 x 4096
 // 10.5 and 12; 64 x 8192 x 8192 17.4 and 19; but 256 x 4096 x 4096 16.1 and 12.0.  Few rows against long ones of many
-// weights are bound by how many loads are under way, and always go here: 64 rows over 32 groups of 4096 x 4096 82 us
-// (5.3 TB/s), 107 to 121 in the tiles; 16 x 16384 x 8192 27 and 36.
+// weights are bound by how many loads are under way, and always go here: 64 rows over 32 groups of 4096 x 4096 79 us
+// (5.4 TB/s), 104 to 121 in the tiles; 16 x 16384 x 8192 27 and 36.  From 32 slabs on, that is; with 31 the tiles take
+// such groups (4096 x 3968: 91 us there, 78 here), and one group of 16 to 32 rows comes here by its estimate as well.
 inline double deep_time_int8(double rows, double cols, double slabs, double groups, bool dma) {
     if (dma && rows <= 32 * groups && slabs >= 32) return 0.0;
     const double high = groups > 1 ? 1.1 * groups * std::max(1.0, rows / groups / 32 + 0.5) : std::ceil(rows / 32);

@@ -10,8 +10,14 @@
 //
 // Measured (a copy reaches 5.2 TB/s here): 8192 x 4096 bf16 in training, 268 MB each way, forward 47 us (5.7 TB/s),
 // backward 50 (5.3) and 5 for the last sum over partial rows; 8192 x 8192 bf16 with a residual to codes with a scale a
-// row, 470 MB, 86 to 91 us (5.2 to 5.5); 5366 x 8176 fp32 135 and 150 us (5.2 and 4.7).  1000 x 777 fp32: 6.7, 6.3
-// and 3.3 us, a launch each and two trips around a wave.  Codes of 8192 x 4096 bf16 18 us (5.6 TB/s).
+// row, 470 MB, 86 to 91 us (5.2 to 5.5), to fp8 97 (4.9); 5366 x 8176 fp32 135 and 150 us (5.2 and 4.7).  1000 x 777
+// fp32: 6.7, 6.5 and 3.3 us: a launch each, the trips to memory of a row's operands, which wait for one another in
+// the forward pass, and two around a wave.  Codes of 8192 x 4096 bf16 18 us (5.6 TB/s).
+//
+// Widths off 8 and between the powers of two are slower: lanes past a row's end idle, and a row's last chunk takes
+// longer (gemm_rows.hpp).  8192 rows bf16, forward and backward with the last sum: 4500 columns (off 8) 121 and 118 us
+// (2.4 and 2.5 TB/s), 6000 86 and 87 (4.6 and 4.5), 9000 129 and 162 (4.6 and 3.7); 5000 x 5000 48 and 58 (4.2 and
+// 3.5), 5000 x 5001 68 and 78.
 #include "gemm_norm.hpp"
 #include "gemm_rows.hpp"
 
@@ -421,8 +427,10 @@ template <int DT, bool LARGE> hipError_t norm_type(const LayerNormParams &p, hip
     return go(&layer_norm_long_kernel<DT>, fold(p.M), 1024, s, p);
 }
 
-// Workgroups of the backward pass: enough to fill the compute units with teams that each still take several
-// rows, so that the partial sums stay a small part of what is moved.
+// Workgroups of the backward pass: enough to fill the compute units.  Their partial sums, 16 bytes a column and
+// workgroup written and read again, are a small part of what is moved from some 4000 rows on.  Of fewer they are
+// more: twice the operator's own bytes for bf16 up to 512 rows of more than 2048 columns (512 x 8192: 67 MB
+// beside 34, 23 us; 1024 x 8192 27, 2048 x 8192 39).
 int grad_workgroups(int64_t M, int64_t N) {
     const int64_t rows = N <= 2048 ? (M + 3) / 4 : M;        // rows a workgroup takes at once: 4, or 1
     return (int)(rows < 512 ? rows : 512);
@@ -458,8 +466,9 @@ int layer_norm_grad_partials(int64_t M, int64_t N) {
     return grad_workgroups(M, N);
 }
 
-// A pass whose operands of this many bytes each cannot stay in the L2 goes past it (8192 x 4096 bf16: forward 51 us
-// and 50 so, backward 57 and 51).
+// A pass whose operands of this many bytes each cannot stay in the L2s accesses them non-temporally.  Without and with,
+// 4096 columns bf16, inputs in turn: 64 MB forward 49 us and 48, backward 55 and 49; 32 MB 28 and 23, 32 and 29; 16 MB
+// 14.7 and 13.4, 16.7 and 17.9.
 static bool large(int64_t M, int64_t N, int32_t dtype) { return (double)M * N * (dtype == GEMM_DTYPE_F32 ? 4 : 2) >= 32 << 20; }
 
 hipError_t launch_layer_norm(const LayerNormParams &p, hipStream_t s) {

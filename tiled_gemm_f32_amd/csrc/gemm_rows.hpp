@@ -47,7 +47,7 @@ template <class V> __device__ __forceinline__ V get(const void *p) {
     return reinterpret_cast<const Anywhere<V> *>(p)->v;
 }
 template <class V> __device__ __forceinline__ void put(void *p, V v) { reinterpret_cast<Anywhere<V> *>(p)->v = v; }
-// The same past the L2, which would hold them until something else pushes them out.
+// The same, non-temporal: a hint to the caches that the lines are not needed again soon.
 template <class V> __device__ __forceinline__ V get_nt(const void *p) {
     typedef V Loose __attribute__((aligned(1)));
     return __builtin_nontemporal_load(static_cast<const Loose *>(p));
@@ -57,7 +57,9 @@ template <class V> __device__ __forceinline__ void put_nt(void *p, V v) {
     __builtin_nontemporal_store(v, static_cast<Loose *>(p));
 }
 
-// Up to 8 values, n of them valid (n <= 0: none; the rest read as zero).
+// Up to 8 values, n of them valid (n <= 0: none; the rest read as zero).  In bf16 the values of a row's last,
+// shorter chunk are loaded one after the other, each waited for before the next: 8192 rows bf16 of 4095 columns
+// take 96 us forward and 146 backward in layer norm, of 4096 49 and 57.
 template <int DT, bool NT = false>
 __device__ __forceinline__ typename Io<DT>::Raw load_raw(const void *base, int64_t at, int n) {
     typedef typename Io<DT>::T T;
