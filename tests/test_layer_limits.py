@@ -1,5 +1,7 @@
 """Sizes next to 2^31 and past it in the calls around the experts.  Nothing here runs a kernel: the calls
 are refused."""
+import ctypes
+
 import pytest
 import torch
 
@@ -43,6 +45,14 @@ def test_negative_counts_past_32_bits_are_invalid(count):
     assert back(top=count) == product(groups=count, ends=PD) == INVALID
     assert grouped(groups=count) == wgrad(groups=count) == INVALID
     assert tg.gemm_expert_plan_workspace_size(100000, 8, count) == 0
+
+
+def test_counts_may_be_ctypes_values():
+    two = ctypes.c_int32(2)
+    assert tg.gemm_expert_plan_workspace_size(100000, two, ctypes.c_int32(64)) == \
+        tg.gemm_expert_plan_workspace_size(100000, 2, 64) > 0
+    assert plan(top=two, ld=1) == dispatch(top=two, ldx=1) == combine(top=two, ldr=1) == back(top=two, lddo=1) == INVALID
+    assert grouped(groups=two, lda=1) == wgrad(groups=two, lddy=1) == product(groups=two, ends=PD, lda=1) == INVALID
 
 
 @pytest.mark.gpu

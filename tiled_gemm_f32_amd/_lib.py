@@ -367,9 +367,9 @@ def gemm_block_scaled(op_b, M, N, K, alpha, A, lda, B, ldb, scales, out_type, ou
 
 def _not_32_bit(*counts) -> int:
     """The status of a call with a count that its 32-bit argument cannot hold, or 0: ctypes would pass on the
-    count's lower bits, which may be a valid one."""
+    count's lower bits, which may be a valid one.  (What is no int, a ctypes value say, is ctypes' to take or not.)"""
     for n in counts:
-        if not -0x80000000 <= n <= 0x7fffffff:
+        if isinstance(n, int) and not -0x80000000 <= n <= 0x7fffffff:
             return GEMM_ERR_UNSUPPORTED if n > 0 else GEMM_ERR_INVALID_ARG
     return GEMM_OK
 
